@@ -324,6 +324,94 @@ soup_status soup_nf4_dequantize(const uint8_t* codes, const int8_t* q8, const fl
 soup_status soup_nf4_matmul(const void* x, int M, int N, int K, const uint8_t* codes, const int8_t* q8,
                             const float* scales, const float* mean, int transpose_w, const void* residual, void* y,
                             void* stream);
+
+/* ---- softmax cross entropy over a large vocabulary, without its logits -------------------- */
+/* The head's loss (guillermodelpino soup.yaml example: task sft) on its own, for vocabularies whose
+ * logits do not fit next to the adapters: l_v = h_t . w_v for the rows t of h [T, hidden] (bf16,
+ * rows ldh elements apart) and the rows v of w [vocab, hidden] (bf16, ldw apart), walked once in
+ * pieces of the vocabulary.  Per row, with targets t1 (and t2, which may be NULL):
+ *   lse[t] = log sum_v exp l_v (may be NULL), logp[t] = l_{t1} - lse, logp2[t] = l_{t2} - lse
+ * (fp32; logp2 is required with t2 and 0 where t2[t] < 0).  A row with t1[t] < 0 has no target: it
+ * costs nothing and its results are 0.  A target >= vocab makes its row one without a target and,
+ * where err is given, sets *err (device int, which the caller zeroes) to a non-zero value.
+ * grad != 0 also leaves in ws what soup_linear_ce_bwd needs.  The gradient is that of
+ * L = -sum_t (weight[t] logp[t] + weight2[t] logp2[t]) with respect to h, for any weights, known
+ * only after the log-probs or not: dh [T, hidden] bf16, rows ldd elements apart:
+ *   dh_t = (w1 + w2) sum_v p_v w_v - w1 w_{t1} - w2 w_{t2}
+ * w is frozen and gets none.  Rows without a target or with zero weights get zeros.
+ * ws: soup_linear_ce_workspace bytes, 256-byte aligned, the caller's own for each call (and the same
+ * one, untouched, for the gradient of that call), so calls on different streams do not meet.  Nothing is
+ * allocated and nothing synchronised: both calls can be captured into a CUDA graph.
+ * SOUP_ERR_UNSUPPORTED unless hidden is a multiple of 8; SOUP_ERR_INVALID_ARG for null pointers,
+ * sizes < 1 (T may be 0: nothing is done), strides below hidden or not multiples of 8, addresses
+ * not 16-byte aligned (ws: 256), ws_bytes below the need.  T below 2^24, hidden up to 2^16, vocab up to 2^22. */
+soup_status soup_linear_ce_workspace(int T, int hidden, int vocab, int grad, size_t* bytes);
+soup_status soup_linear_ce_fwd(const void* h, long long ldh, const void* w, long long ldw, int T, int hidden, int vocab,
+                               const int32_t* t1, const int32_t* t2, int grad, float* lse, float* logp, float* logp2,
+                               void* ws, size_t ws_bytes, int* err, void* stream);
+soup_status soup_linear_ce_bwd(const void* w, long long ldw, int T, int hidden, int vocab, const float* weight,
+                               const float* weight2, void* dh, long long ldd, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- AdamW over many tensors -------------------------------------------------------------- */
+/* The trained adapters' update (guillermodelpino soup.yaml example: lr) for any set of tensors in as
+ * few launches as descriptors fit (one up to 640 tensors), with states in 32 or in 8 bits:
+ *   m' = b1 m + (1-b1) g, v' = b2 v + (1-b2) g^2, p' = p - lr (m' c1 / (sqrt(v' c2) + eps) + wd p),
+ *   c = 1 / (1 - b^step)
+ * States lie one tensor after the other, each from a whole block of SOUP_ADAMW_BLOCK elements on;
+ * soup_adamw_state_numel adds that up.  m_scale == NULL: m, v are fp32.  Otherwise m is int8 and v
+ * uint8 with one fp32 scale a block (the block's largest |m'|, v'), standing for
+ *   m = m_scale sign(q) (q/127)^2,  v = v_scale (q/255)^4  (v > 0 is coded as 1 at least);
+ * a zero state is all zeros either way.  Arithmetic is fp32 whatever the types; p (fp32 or bf16) is
+ * rounded once.  p_bf16_copy (may be NULL) receives p' rounded to bf16.  hp (device float[3], may be NULL):
+ * lr, 1/(1-b1^step), 1/(1-b2^step) read on the device in place of lr and step, for captured graphs.
+ * tensors is a host array, read during the call.  A tensor of n = 0 is allowed.  SOUP_ERR_INVALID_ARG
+ * for null pointers, n < 0, step < 1 (without hp), v_scale without m_scale or the reverse, a
+ * state address not 16-byte aligned, or tensors not aligned to their own type. */
+#define SOUP_ADAMW_BLOCK 256
+typedef struct soup_adamw_tensor {
+  void* p;               /* device, n elements, updated in place */
+  const void* g;         /* device, n elements */
+  uint16_t* p_bf16_copy; /* device, n elements, or NULL */
+  long long n;
+} soup_adamw_tensor;
+typedef struct soup_adamw_options {
+  int params_bf16, grads_bf16; /* 0: fp32 */
+  int step; /* from 1 */
+  double lr, beta1, beta2, eps, weight_decay; /* double: 1 - beta2 is formed before fp32 sees it */
+} soup_adamw_options;
+soup_status soup_adamw_state_numel(const soup_adamw_tensor* tensors, int count, long long* numel);
+soup_status soup_adamw_multi(const soup_adamw_tensor* tensors, int count, const soup_adamw_options* opt, void* m, void* v,
+                             float* m_scale, float* v_scale, const float* hp, void* stream);
+/* What 8-bit states stand for, in bf16: n elements (a multiple of SOUP_ADAMW_BLOCK) each. */
+soup_status soup_adamw_state_values(const void* m, const void* v, const float* m_scale, const float* v_scale, long long n,
+                                    uint16_t* m_out, uint16_t* v_out, void* stream);
+
+/* ---- rotary positions --------------------------------------------------------------------- */
+/* Rotary embedding of q [T, heads_q, head_dim] and k [T, heads_k, head_dim] (heads contiguous, tokens
+ * ldq / ldk elements apart; k may be NULL with heads_k = 0), out of place or in place (out == in with
+ * the same stride): the first rotary_dim values of each head are rotated by position x frequency.
+ * interleaved = 0 pairs (i, i + rotary_dim/2), 1 pairs (2i, 2i + 1).  Frequencies are
+ * theta^(-2i/rotary_dim), scaled for contexts beyond the trained one:
+ *   LINEAR  f / factor                       NTK     theta x factor^(d/(d-2))
+ *   BY_PARTS (the long-context scaling of the Llama-3.1 shape): with r = original_len f / 2 pi turns
+ *           in the trained context and g = clamp((r - low) / (high - low), 0, 1): g f + (1-g) f / factor
+ *   YARN (Peng et al. 2023): as BY_PARTS, and cos, sin times 1 + 0.1 ln factor
+ * inverse != 0 applies the transpose, which is the gradient.  dtype 0: bf16, 1: fp32; angles are formed in
+ * 64 bits and the result rounded once.  positions: device int32 [T].  The library's own decoder
+ * layers take the same configuration (soup_model_config.rope).  SOUP_ERR_INVALID_ARG for a bad
+ * configuration, null pointers, strides below heads x head_dim, or addresses not aligned to the type;
+ * SOUP_ERR_UNSUPPORTED for rotary_dim odd, above head_dim or above 256.  T = 0 does nothing. */
+enum { SOUP_ROPE_NONE = 0, SOUP_ROPE_LINEAR, SOUP_ROPE_NTK, SOUP_ROPE_BY_PARTS, SOUP_ROPE_YARN };
+typedef struct soup_rope_config {
+  int rotary_dim, interleaved, scaling, original_len;
+  double theta, factor, low_freq_factor, high_freq_factor;
+} soup_rope_config;
+/* Host only: the rotary_dim / 2 frequencies (radians a position) and the factor on cos and sin. */
+soup_status soup_rope_frequencies(const soup_rope_config* cfg, double* freq, double* factor_on_cos_sin);
+soup_status soup_rope(const soup_rope_config* cfg, const void* q, long long ldq, void* q_out, long long ldq_out, int heads_q,
+                      const void* k, long long ldk, void* k_out, long long ldk_out, int heads_k, int head_dim, int T,
+                      const int32_t* positions, int dtype, int inverse, void* stream);
+
 /* ---- GEMM scheduling diagnostics (host only: no GPU needed, nothing launched) ----------- */
 /* How the library schedules y[M, N] = x[M, K] . W^T for one operand W: nf4 != 0 for an NF4
  * weight (transposed != 0: the dX orientation, W read as [K, N]), else bf16; with the

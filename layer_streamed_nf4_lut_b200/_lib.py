@@ -20,6 +20,8 @@ SOUP_RESIDENT, SOUP_STREAMED = 0, 1
 SOUP_SOURCE_RAM, SOUP_SOURCE_FILE, SOUP_SOURCE_AUTO = 0, 1, 2
 SOUP_LOSS_SFT, SOUP_LOSS_DPO, SOUP_LOSS_KTO, SOUP_LOSS_ORPO, SOUP_LOSS_SIMPO = 0, 1, 2, 3, 4
 LOSS_KINDS = {"sft": 0, "dpo": 1, "kto": 2, "orpo": 3, "simpo": 4}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4}
+ADAMW_BLOCK = 256  # SOUP_ADAMW_BLOCK
 PROJ = ("q", "k", "v", "o", "gate", "up", "down")
 
 
@@ -62,6 +64,22 @@ class GemmPlanInfo(Structure):
                 ("stream_k_tiles", c_int), ("stream_k_tiles_m", c_int), ("stream_k_kblocks", c_int)]
 
 
+class AdamwOptions(Structure):
+    _fields_ = [("params_bf16", c_int), ("grads_bf16", c_int), ("step", c_int), ("lr", ctypes.c_double),
+                ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("weight_decay", ctypes.c_double)]
+
+
+class AdamwTensor(Structure):
+    _fields_ = [("p", c_void_p), ("g", c_void_p), ("p_bf16_copy", c_void_p), ("n", c_longlong)]
+
+
+class RopeConfig(Structure):
+    _fields_ = [("rotary_dim", c_int), ("interleaved", c_int), ("scaling", c_int), ("original_len", c_int),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("low_freq_factor", ctypes.c_double),
+                ("high_freq_factor", ctypes.c_double)]
+
+
 class Batch(Structure):
     _fields_ = [("ids", c_void_p), ("loss_mask", c_void_p), ("B", c_int), ("S", c_int), ("ids_on_host", c_int),
                 ("n_pairs", c_int), ("prefix_len", c_int), ("beta", c_float), ("lr", c_float),
@@ -99,6 +117,18 @@ SIGNATURES = {
     "soup_nf4_matmul": [c_void_p, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p,
                         c_void_p, c_void_p],
     "soup_nf4_codebook": [POINTER(c_float)],
+    "soup_linear_ce_workspace": [c_int, c_int, c_int, c_int, POINTER(c_size_t)],
+    "soup_linear_ce_fwd": [c_void_p, c_longlong, c_void_p, c_longlong, c_int, c_int, c_int, c_void_p, c_void_p, c_int,
+                           c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p],
+    "soup_linear_ce_bwd": [c_void_p, c_longlong, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_longlong,
+                           c_void_p, c_size_t, c_void_p],
+    "soup_adamw_state_numel": [c_void_p, c_int, POINTER(c_longlong)],
+    "soup_adamw_multi": [c_void_p, c_int, POINTER(AdamwOptions), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                         c_void_p],
+    "soup_adamw_state_values": [c_void_p, c_void_p, c_void_p, c_void_p, c_longlong, c_void_p, c_void_p, c_void_p],
+    "soup_rope_frequencies": [POINTER(RopeConfig), POINTER(ctypes.c_double), POINTER(ctypes.c_double)],
+    "soup_rope": [POINTER(RopeConfig), c_void_p, c_longlong, c_void_p, c_longlong, c_int, c_void_p, c_longlong, c_void_p,
+                  c_longlong, c_int, c_int, c_int, c_void_p, c_int, c_int, c_void_p],
     "soup_get_stats": [c_void_p, POINTER(Stats)],
     "soup_reset_stats": [c_void_p],
     "soup_check_device": [c_void_p, c_void_p],

@@ -1704,6 +1704,19 @@ bool tma_encode_bf16_sw128(CUtensorMap* map, const void* ptr, unsigned long long
                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool tma_encode_sw128(CUtensorMap* map, const void* ptr, bool f32, unsigned long long inner, unsigned long long outer,
+                      unsigned long long row_bytes, unsigned box_inner, unsigned box_outer) {
+  const auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer}, strides[1] = {row_bytes};
+  cuuint32_t box[2] = {box_inner, box_outer}, es[2] = {1, 1};
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr),
+            dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int device_sm_count() { return sm_count(); }
+
 GemmPlan gemm_plan(const GemmParams& p, int sms, bool stream_k_allowed) {
   GemmPlan pl{};
   if (sms < 1) sms = 148;

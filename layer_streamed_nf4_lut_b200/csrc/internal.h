@@ -6,6 +6,9 @@
 #include <stddef.h>
 
 #include <atomic>
+#include <string>
+
+#include "soup.h"
 
 namespace soup {
 
@@ -114,6 +117,12 @@ struct GemmParams {
 // Cached by its arguments.  False if the driver refuses it (alignment, sizes).
 bool tma_encode_bf16_sw128(CUtensorMap* map, const void* ptr, unsigned long long inner, unsigned long long outer,
                            unsigned long long row_bytes, unsigned box_inner, unsigned box_outer);
+
+// The same for bf16 or fp32 (box_inner times the element size must be 128), encoded afresh each
+// time: for addresses that change from call to call.
+bool tma_encode_sw128(CUtensorMap* map, const void* ptr, bool f32, unsigned long long inner, unsigned long long outer,
+                      unsigned long long row_bytes, unsigned box_inner, unsigned box_outer);
+int device_sm_count();  // SMs of the current device
 
 // The same array seen as 64-element column blocks ("planes", 128 B apart) of `rows` rows: a
 // 3D map (64, rows, planes) whose box (64, box_rows, box_planes) lands in shared memory as
@@ -269,6 +278,39 @@ cudaError_t null_launch(cudaStream_t st);
 cudaError_t bounded_wait_selftest_launch(int* err, unsigned long long limit_ns, cudaStream_t st);                           // profiling aid, not counted as a launch
 cudaError_t f32_to_bf16_launch(const float* x, uint16_t* y, long long n, cudaStream_t st);
 cudaError_t fill_zero_launch(void* p, size_t bytes, cudaStream_t st);
+
+// ----------------------------------------------------------------- loss over the vocabulary in pieces
+// linear_ce.cu.  ws: linear_ce_workspace(T, H, V, grad) bytes, 256-byte aligned; a gradient call reads
+// what the forward call with grad left there.
+size_t linear_ce_workspace(int T, int H, int V, bool grad);
+cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_t* w, long long ldw, int T, int H, int V,
+                                 const int32_t* t1, const int32_t* t2, bool grad, float* lse, float* logp, float* logp2,
+                                 uint8_t* ws, int* err, cudaStream_t st);
+cudaError_t linear_ce_bwd_launch(const uint16_t* w, long long ldw, int T, int H, int V, const float* weight,
+                                 const float* weight2, uint16_t* dh, long long ldd, uint8_t* ws, cudaStream_t st);
+
+// ----------------------------------------------------------------- rotary positions
+constexpr int ROPE_MAX_PAIRS = 128;
+struct RopeCall {
+  const void* x[2];
+  void* y[2];
+  long long ldx[2], ldy[2];
+  int heads[2];
+  int head_dim, rotary, T, f32, interleaved, back;
+  const int32_t* positions;
+  float grow;
+  const double* freq;  // host, rotary / 2
+};
+cudaError_t rope_launch(const RopeCall& c, cudaStream_t st);
+bool rope_config_ok(const soup_rope_config& c, std::string& why);
+void rope_frequencies(const soup_rope_config& c, double* freq, double* grow);  // freq: rotary_dim / 2
+
+// ----------------------------------------------------------------- AdamW over many tensors
+constexpr int ADAMW_BLOCK = 256;  // elements that share a scale of an 8-bit state
+cudaError_t adamw_multi_launch(const soup_adamw_tensor* tensors, int count, const soup_adamw_options& o, void* m, void* v,
+                               float* m_scale, float* v_scale, const float* hp, cudaStream_t st);
+cudaError_t adamw_values_launch(const uint8_t* m, const uint8_t* v, const float* m_scale, const float* v_scale, long long n,
+                                uint16_t* mo, uint16_t* vo, cudaStream_t st);
 
 // ----------------------------------------------------------------- launch accounting
 // Number of kernels this library has launched (process-wide, monotonically increasing).

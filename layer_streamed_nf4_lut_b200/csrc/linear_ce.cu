@@ -1,0 +1,728 @@
+// Softmax cross entropy of h W^T over a large vocabulary, in pieces of the vocabulary, without
+// keeping the logits, with the gradient of h (sm_100a).
+//
+// Mathematics.  Row t with target y and logits l_v = h_t . W_v (in units of log 2 below):
+//   other = sum_{v != y} 2^(l_v - ref),  Z = other + 2^(l_y - ref),  logp = log(2^(l_y - ref) / Z)
+//   dh_t  = w (1/Z) sum_{v != y} 2^(l_v - ref) W_v  -  w (other / Z) W_y
+// The target's column stays out of the product and its coefficient 1 - p_y is formed from `other`,
+// so a row whose target has nearly all the probability keeps a gradient of full relative
+// accuracy.  A row may have a second target (the last prefix row of a shared-prefix preference
+// pair): both columns stay out, each with its own coefficient.
+//
+// The sum over v needs no final Z, so the vocabulary is walked once: per piece, one GEMM turns
+// h W_piece^T into P = 2^(l - ref) (bf16) in its epilogue, and a second GEMM adds P W_piece to an
+// fp32 accumulator.  4 T V H flops in all, nothing is computed twice.  `ref` is a whole number
+// (the target's logit, rounded): a rescaling by a difference of two refs is a power of two and
+// therefore exact.  bf16 has the exponent range of fp32, so ref need not be the row's
+// maximum, only within REF_ROOM powers of two below it; a tile that finds a larger logit stores its
+// values against a ref of its own and raises a flag, and `ce_raise_kernel` brings the row's P and
+// accumulator to the larger ref before the second GEMM reads them.
+//
+// Rows without a target (target < 0) take no part: `ce_prepare_kernel` packs the others' hidden
+// states, so a half-masked batch costs half.
+#include "common.cuh"
+#include "internal.h"
+#include "tc.cuh"
+
+#include <algorithm>
+#include <cstring>
+
+namespace soup {
+
+namespace {
+
+constexpr int TILE = 256;            // rows and columns of a CTA pair's output tile
+constexpr int BK = 64;               // k-block: 64 bf16 = one 128-byte swizzle row
+constexpr int STAGES = 6;            // operand ring
+constexpr int OPERAND = 128 * 128;   // bytes of one operand's k-block in one CTA (128 rows x 64 bf16)
+constexpr int STAGE_BYTES = 2 * OPERAND;
+constexpr int STAGING = 2 * 16384;   // epilogue: two boxes of 128 rows x 128 bytes
+constexpr int BARRIERS = 256;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING + BARRIERS + 1024;
+constexpr int THREADS = 256;         // warp 0 TMA, 1 MMA, 2 TMEM, 3 idle, 4-7 epilogue
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float REF_ROOM = 80.f;     // a logit may exceed its row's ref by this many powers of two:
+                                     // sums stay below 2^(80 + 17) and products with W below fp32's 2^128
+
+struct CeGemm {
+  CUtensorMap ta, tb, to;
+  const int* n_rows;  // rows in use (device)
+  int n_tiles;        // output tiles of 256 columns
+  int kb;             // k-blocks
+  int splits;         // gradient: K ranges, each with an accumulator of its own
+  int tcap;           // rows of one accumulator / of a part_* column
+  int cols;           // columns in use
+  int accumulate;     // gradient: add to the accumulator instead of writing it
+  int w_row0;         // first row of W of this piece
+  const int2* target; // per packed row: the targets' columns (-1: none)
+  const float* ref;
+  float *part_s, *part_r;  // [vocabulary tile][tcap]: the tile's sum and the ref it is against
+  int tile0;          // first vocabulary tile of this piece
+  int store_p;
+  int* raised;
+  int* err;
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// the same, telling every epilogue thread whether all of them have `ok` (a wait that gave up in one
+// thread ends the loop for all, so that none is left alone at a barrier)
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  int all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<int>(ok))
+      : "memory");
+  return all != 0;
+}
+
+// One output tile of a persistent CTA pair's list.
+struct Unit {
+  int m, n, split, kb_lo, kb_hi;
+};
+template <bool GRAD>
+__device__ __forceinline__ Unit unit_of(const CeGemm& p, int m_tiles, int u) {
+  Unit t;
+  t.m = u % m_tiles;
+  const int r = u / m_tiles;
+  t.n = r % p.n_tiles;
+  t.split = GRAD ? r / p.n_tiles : 0;
+  t.kb_lo = GRAD ? static_cast<int>(static_cast<long long>(p.kb) * t.split / p.splits) : 0;
+  t.kb_hi = GRAD ? static_cast<int>(static_cast<long long>(p.kb) * (t.split + 1) / p.splits) : p.kb;
+  return t;
+}
+
+// 256 x 256 tiles, one CTA pair each (tcgen05 cta_group::2, M = 256, N = 256), two accumulators
+// in tensor memory so that a tile's epilogue runs beside the next tile's products.
+// GRAD = false: logits tile -> P, sums.  GRAD = true: P W -> accumulator.
+template <bool GRAD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_kernel(const __grid_constant__ CeGemm p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* staging = smem + STAGES * STAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + STAGING);
+  uint64_t* full = bars;                 // [STAGES]; the first CTA's are used
+  uint64_t* empty = bars + STAGES;       // [STAGES]; each CTA's own
+  uint64_t* acc_full = bars + 2 * STAGES;       // [2]; each CTA's own
+  uint64_t* acc_empty = bars + 2 * STAGES + 2;  // [2]; the first CTA's are used
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);  // four epilogue warps in each CTA
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int rows = *p.n_rows;
+  const int m_tiles = (rows + TILE - 1) / TILE;
+  const int units = m_tiles * p.n_tiles * (GRAD ? p.splits : 1);
+
+  if (warp == 0 && lane == 0) {
+    // ---- operand loads: this CTA's 128 rows of A and its half of B's 256 columns
+    int it = 0;
+    for (int u = pair; u < units; u += pairs) {
+      const Unit t = unit_of<GRAD>(p, m_tiles, u);
+      const int m0 = t.m * TILE + rank * 128, n0 = t.n * TILE + rank * 128;
+      for (int kb = t.kb_lo; kb < t.kb_hi; ++kb, ++it) {
+        const int s = it % STAGES;
+        if (it >= STAGES && !mbar_wait_bounded(&empty[s], ((it / STAGES) - 1) & 1, abort_flag, p.err)) goto done;
+        uint8_t* a = smem + s * STAGE_BYTES;
+        uint8_t* b = a + OPERAND;
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
+        const uint32_t bar = cluster_addr(&full[s], 0);
+        tma_load_2d_pair(a, &p.ta, kb * BK, m0, bar);
+        if (GRAD) {
+          tma_load_2d_pair(b, &p.tb, n0, p.w_row0 + kb * BK, bar);
+          tma_load_2d_pair(b + 8192, &p.tb, n0 + 64, p.w_row0 + kb * BK, bar);
+        } else {
+          tma_load_2d_pair(b, &p.tb, kb * BK, p.w_row0 + n0, bar);
+        }
+      }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---- products of both CTAs
+    const uint32_t idesc = idesc_bf16(TILE, TILE, false, GRAD);
+    int it = 0, n_done = 0;
+    for (int u = pair; u < units; u += pairs) {
+      const Unit t = unit_of<GRAD>(p, m_tiles, u);
+      if (t.kb_lo == t.kb_hi) continue;
+      const int b = n_done & 1;
+      if (n_done >= 2 && !mbar_wait_bounded(&acc_empty[b], ((n_done >> 1) - 1) & 1, abort_flag, p.err)) goto done;
+      tc_fence_after();
+      for (int kb = t.kb_lo; kb < t.kb_hi; ++kb, ++it) {
+        const int s = it % STAGES;
+        if (!mbar_wait_bounded(&full[s], (it / STAGES) & 1, abort_flag, p.err)) goto done;
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + s * STAGE_BYTES);
+        const uint64_t da = sw128_kmajor_desc(a);
+        const uint64_t db = GRAD ? sw128_mnmajor_desc(a + OPERAND) : sw128_kmajor_desc(a + OPERAND);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma_f16_pair(tmem + b * TILE, da + k * (32 >> 4), db + k * ((GRAD ? 2048 : 32) >> 4), idesc,
+                          (kb > t.kb_lo || k > 0) ? 1u : 0u);
+        tc_commit_pair(&empty[s]);
+      }
+      tc_commit_pair(&acc_full[b]);
+      ++n_done;
+    }
+  } else if (warp >= 4) {
+    // ---- epilogue: thread = accumulator row
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint8_t* my_row[2] = {staging + row * 128, staging + 16384 + row * 128};
+    const bool elected = threadIdx.x == 128;
+    int n_done = 0, boxes = 0;
+    for (int u = pair; u < units; u += pairs) {
+      const Unit t = unit_of<GRAD>(p, m_tiles, u);
+      if (t.kb_lo == t.kb_hi) continue;
+      const int b = n_done & 1;
+      if (!epilogue_all(mbar_wait_bounded(&acc_full[b], (n_done >> 1) & 1, abort_flag, p.err))) goto done;
+      tc_fence_after();
+      const uint32_t acc = tmem + lanes + b * TILE;
+      const int m0 = t.m * TILE + rank * 128, n0 = t.n * TILE;
+      if (GRAD) {
+        for (int c = 0; c < TILE; c += 32, ++boxes) {
+          uint32_t v[32];
+          tmem_ld32(acc + c, v);
+          tmem_ld_wait();
+          if (elected) tma_store_wait_read<1>();
+          epilogue_sync();
+          uint8_t* dst = my_row[boxes & 1];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(dst + ((j ^ (row & 7)) << 4)) =
+                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          fence_proxy_async_smem();
+          epilogue_sync();
+          if (elected && n0 + c < p.cols) {
+            const uint8_t* src = staging + (boxes & 1) * 16384;
+            if (p.accumulate)
+              tma_reduce_add_2d(&p.to, n0 + c, t.split * p.tcap + m0, src);
+            else
+              tma_store_2d(&p.to, n0 + c, t.split * p.tcap + m0, src);
+          }
+          if (elected) tma_store_commit();
+        }
+      } else {
+        const int r = m0 + row;
+        const bool live = r < rows;
+        int2 tg = live ? p.target[r] : make_int2(-1, -1);  // columns of this piece (others: out of range)
+        tg.x -= p.w_row0;
+        tg.y -= p.w_row0;
+        float ref = live ? p.ref[r] : 0.f;
+        const int valid = p.cols - n0;  // columns of this tile inside the vocabulary
+        // the largest logit that takes part: only to see whether ref has room for it
+        float mx = -INFINITY;
+        for (int c = 0; c < TILE; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(acc + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int col = c + j;
+            const float x = (col < valid && n0 + col != tg.x && n0 + col != tg.y) ? __uint_as_float(v[j]) : -INFINITY;
+            mx = fmaxf(mx, x);
+          }
+        }
+        mx *= LOG2E;
+        if (live && mx - ref > REF_ROOM) {
+          ref = ceilf(mx);
+          *p.raised = 1;
+        }
+        __syncwarp();
+        float sum = 0.f;
+        for (int c = 0; c < TILE; c += 64, ++boxes) {
+          uint32_t w[32];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t v[32];
+            tmem_ld32(acc + c + 32 * half, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float e[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int col = c + 32 * half + j + k;
+                e[k] = exp2_approx(fmaf(__uint_as_float(v[j + k]), LOG2E, -ref));
+                if (col >= valid || n0 + col == tg.x || n0 + col == tg.y) e[k] = 0.f;
+                sum += e[k];
+              }
+              w[16 * half + (j >> 1)] = pack_bf16x2(e[0], e[1]);
+            }
+          }
+          if (p.store_p) {
+            if (elected) tma_store_wait_read<1>();
+            epilogue_sync();
+            uint8_t* dst = my_row[boxes & 1];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(dst + ((j ^ (row & 7)) << 4)) =
+                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            fence_proxy_async_smem();
+            epilogue_sync();
+            if (elected) {
+              tma_store_2d(&p.to, n0 + c, m0, staging + (boxes & 1) * 16384);
+              tma_store_commit();
+            }
+          }
+        }
+        const long long at = static_cast<long long>(p.tile0 + t.n) * p.tcap + r;
+        p.part_s[at] = sum;
+        p.part_r[at] = ref;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[b], 0));
+      ++n_done;
+    }
+    if (elected) tma_store_wait_all();
+  }
+done:
+  __syncwarp();
+  if (*abort_flag) {  // a wait gave up: let this CTA's copies in flight land before its memory goes
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- rows
+struct CeRows {  // per packed row
+  int2* target;
+  int* row;              // its row in the batch
+  float *ref, *la, *lb;  // ref and the targets' logits, in powers of two
+  float* inv_z;          // once the vocabulary is done: 1 / Z against ref,
+  float2 *pa, *pb;       // and each target's p and 1 - p
+};
+
+__device__ __forceinline__ int2 targets_of(const int32_t* t1, const int32_t* t2, int t, int V, int* err) {
+  int a = t1[t], b = t2 ? t2[t] : -1;
+  if (a >= V || b >= V) {
+    if (err) set_dev_error(err, DEVERR_BOUNDS);
+    return make_int2(-1, -1);
+  }
+  if (a < 0) return make_int2(-1, -1);
+  return make_int2(a, b < 0 ? -1 : b);
+}
+
+// One block per row: a row's place among the rows with targets is the count of those before it (the
+// whole list of targets is a few KB, read from the L2).  Packs the row's hidden state and forms the
+// targets' logits in fp32.
+__global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh, const uint16_t* __restrict__ w,
+                                  long long ldw, int T, int H, int V, const int32_t* __restrict__ t1,
+                                  const int32_t* __restrict__ t2, uint16_t* __restrict__ packed, CeRows rows,
+                                  int* __restrict__ place, int* __restrict__ n_rows, int* __restrict__ raised, int pieces,
+                                  float* __restrict__ lse, float* __restrict__ logp, float* __restrict__ logp2, int* err) {
+  __shared__ float red[32];
+  __shared__ int before;
+  const int t = blockIdx.x;
+  if (threadIdx.x == 0) before = 0;
+  __syncthreads();
+  int n = 0;
+  for (int i = threadIdx.x; i < t; i += blockDim.x) n += targets_of(t1, t2, i, V, nullptr).x >= 0;
+  n = __reduce_add_sync(0xffffffffu, n);
+  if ((threadIdx.x & 31) == 0 && n) atomicAdd(&before, n);
+  if (t == 0)
+    for (int i = threadIdx.x; i < pieces; i += blockDim.x) raised[i] = 0;
+  __syncthreads();
+  const int2 tg = targets_of(t1, t2, t, V, threadIdx.x == 0 ? err : nullptr);
+  const int at = before;
+  if (t == T - 1 && threadIdx.x == 0) *n_rows = at + (tg.x >= 0);
+  if (tg.x < 0) {
+    if (threadIdx.x == 0) {
+      place[t] = -1;
+      if (lse) lse[t] = 0.f;
+      logp[t] = 0.f;
+      if (logp2) logp2[t] = 0.f;
+    }
+    return;
+  }
+  const uint16_t* hr = h + t * ldh;
+  const uint16_t* wa = w + tg.x * ldw;
+  const uint16_t* wb = w + (tg.y >= 0 ? tg.y : tg.x) * ldw;
+  float a = 0.f, b = 0.f;
+  for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
+    const uint4 hv = *reinterpret_cast<const uint4*>(hr + c);
+    const uint4 av = *reinterpret_cast<const uint4*>(wa + c);
+    const uint4 bv = *reinterpret_cast<const uint4*>(wb + c);
+    *reinterpret_cast<uint4*>(packed + static_cast<long long>(at) * H + c) = hv;
+    const uint32_t hw[4] = {hv.x, hv.y, hv.z, hv.w}, aw[4] = {av.x, av.y, av.z, av.w}, bw[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = unpack_bf16x2(hw[j]), y = unpack_bf16x2(aw[j]), z = unpack_bf16x2(bw[j]);
+      a += x.x * y.x + x.y * y.y;
+      b += x.x * z.x + x.y * z.y;
+    }
+  }
+  a = block_sum(a, red);
+  b = block_sum(b, red);
+  if (threadIdx.x == 0) {
+    place[t] = at;
+    a *= LOG2E;
+    b *= LOG2E;
+    rows.target[at] = tg;
+    rows.row[at] = t;
+    rows.la[at] = a;
+    rows.lb[at] = b;
+    rows.ref[at] = rintf(tg.y >= 0 ? fmaxf(a, b) : a);
+  }
+}
+
+// Rows that met a logit beyond their ref's room: P of this piece and the accumulators go to the
+// largest ref a tile took.  Powers of two: exact.  One warp per row; nothing to do while the
+// piece's flag is down.
+__global__ void ce_raise_kernel(const int* __restrict__ raised, const int* __restrict__ n_rows, int tile0, int tiles,
+                                int tcap, const float* __restrict__ part_r, float* __restrict__ ref,
+                                uint16_t* __restrict__ P, long long ldp, float* __restrict__ acc, int splits, int H,
+                                int accumulated) {
+  if (*raised == 0) return;
+  const int lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x >> 5);
+  for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < *n_rows; r += warps) {
+    float top = ref[r];
+    for (int i = lane; i < tiles; i += 32) top = fmaxf(top, part_r[static_cast<long long>(tile0 + i) * tcap + r]);
+    top = warp_max(top);
+    if (!(top > ref[r])) continue;
+    for (int i = 0; i < tiles; ++i) {
+      const float have = part_r[static_cast<long long>(tile0 + i) * tcap + r];
+      if (have == top) continue;
+      const float f = exp2f(have - top);
+      uint16_t* q = P + r * ldp + i * TILE;
+      for (int c = lane; c < TILE; c += 32) {
+        const __nv_bfloat16 v = __float2bfloat16_rn(bf16_to_f32(q[c]) * f);
+        q[c] = *reinterpret_cast<const uint16_t*>(&v);
+      }
+    }
+    if (accumulated) {
+      const float f = exp2f(ref[r] - top);
+      for (int s = 0; s < splits; ++s) {
+        float* a = acc + (static_cast<long long>(s) * tcap + r) * H;
+        for (int c = lane; c < H; c += 32) a[c] *= f;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) ref[r] = top;
+  }
+}
+
+// Sums of each row's tiles (32 rows per block: lane = row, the warps share the tiles and their sums
+// are added in warp order), log-probs and lse.  The scalars of a row are formed in 64 bits.
+__global__ void ce_stats_kernel(const int* __restrict__ n_rows, int tiles, int tcap, const float* __restrict__ part_s,
+                                const float* __restrict__ part_r, CeRows rows, float* __restrict__ out_lse,
+                                float* __restrict__ out_logp, float* __restrict__ out_logp2) {
+  __shared__ float sums[8][32], refs[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.x * 32 + lane;
+  const bool live = r < *n_rows;
+  float top = -INFINITY, sum = 0.f;
+  if (live) {
+    top = rows.ref[r];
+    for (int i = warp; i < tiles; i += 8) {
+      const long long at = static_cast<long long>(i) * tcap + r;
+      const float s = part_s[at], k = part_r[at];
+      if (k > top) {
+        sum *= exp2f(top - k);
+        top = k;
+      }
+      sum += s * exp2f(k - top);
+    }
+  }
+  sums[warp][lane] = sum;
+  refs[warp][lane] = top;
+  __syncthreads();
+  if (warp != 0 || !live) return;
+  for (int i = 1; i < 8; ++i) top = fmaxf(top, refs[i][lane]);
+  double other = 0.0;
+  for (int i = 0; i < 8; ++i) other += static_cast<double>(sums[i][lane]) * exp2(static_cast<double>(refs[i][lane] - top));
+  const int2 tg = rows.target[r];
+  const bool two = tg.y >= 0 && tg.y != tg.x;
+  const double ln2 = 0.6931471805599453;
+  const double a = static_cast<double>(rows.la[r]) - top, b = static_cast<double>(rows.lb[r]) - top;
+  const double ea = exp2(a), eb = two ? exp2(b) : 0.0;
+  const double z = other + ea + eb, lz = log(z);
+  const double rest_a = other + eb, rest_b = other + ea;
+  const double lpa = ea > rest_a ? -log1p(rest_a / ea) : a * ln2 - lz;
+  const double lpb = two ? (eb > rest_b ? -log1p(rest_b / eb) : b * ln2 - lz) : lpa;
+  rows.inv_z[r] = static_cast<float>(1.0 / z);
+  rows.pa[r] = make_float2(static_cast<float>(ea / z), static_cast<float>(rest_a / z));
+  rows.pb[r] = make_float2(static_cast<float>(eb / z), static_cast<float>(rest_b / z));
+  const int t = rows.row[r];
+  if (out_lse) out_lse[t] = static_cast<float>(static_cast<double>(top) * ln2 + lz);
+  out_logp[t] = static_cast<float>(lpa);
+  if (out_logp2) out_logp2[t] = tg.y >= 0 ? static_cast<float>(lpb) : 0.f;
+}
+
+// dh of one row of the batch per block: the accumulators of the K ranges, added in order, and the
+// targets' rows of W with coefficients formed from 1 - p.
+__global__ void ce_dh_kernel(const int* __restrict__ place, CeRows rows, const float* __restrict__ weight,
+                             const float* __restrict__ weight2, const float* __restrict__ acc, int splits, int tcap,
+                             const uint16_t* __restrict__ w, long long ldw, int H, uint16_t* __restrict__ dh,
+                             long long ldd) {
+  const int t = blockIdx.x;
+  uint16_t* out = dh + t * ldd;
+  const int r = place[t];
+  int2 tg = make_int2(-1, -1);
+  float w1 = 0.f, w2 = 0.f;
+  if (r >= 0) {
+    tg = rows.target[r];
+    w1 = weight[t];
+    if (tg.y >= 0 && weight2) w2 = weight2[t];
+  }
+  if (w1 == 0.f && w2 == 0.f) {
+    for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const float2 pa = rows.pa[r], pb = rows.pb[r];
+  const bool two = tg.y >= 0 && tg.y != tg.x;
+  const float k = (w1 + w2) * rows.inv_z[r];
+  const float ca = two ? w2 * pa.x - w1 * pa.y : -(w1 + w2) * pa.y;
+  const float cb = two ? w1 * pb.x - w2 * pb.y : 0.f;
+  const uint16_t* wa = w + tg.x * ldw;
+  const uint16_t* wb = w + (two ? tg.y : tg.x) * ldw;
+  for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    for (int s = 0; s < splits; ++s) {
+      const float4* q = reinterpret_cast<const float4*>(acc + (static_cast<long long>(s) * tcap + r) * H + c);
+      const float4 x = q[0], y = q[1];
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    const uint4 av = *reinterpret_cast<const uint4*>(wa + c);
+    const uint4 bv = *reinterpret_cast<const uint4*>(wb + c);
+    const uint32_t aw[4] = {av.x, av.y, av.z, av.w}, bw[4] = {bv.x, bv.y, bv.z, bv.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = unpack_bf16x2(aw[j]), y = unpack_bf16x2(bw[j]);
+      const float lo = k * v[2 * j] + ca * x.x, hi = k * v[2 * j + 1] + ca * x.y;
+      o[j] = two ? pack_bf16x2(lo + cb * y.x, hi + cb * y.y) : pack_bf16x2(lo, hi);
+    }
+    *reinterpret_cast<uint4*>(out + c) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// ---------------------------------------------------------------- the plan
+constexpr int ROW_BLOCK = 4096;                       // rows that share one walk over the vocabulary
+constexpr long long P_BYTES = 64ll << 20;             // of one piece's P: half of the L2
+constexpr int MAX_SPLITS = 4;
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+struct CePlan {
+  int block, blocks, tcap, tiles, piece_tiles, pieces, splits;
+  // byte offsets: per row block (stride per_block), then shared by the blocks
+  size_t n_rows, place, target, row, ref, la, lb, inv_z, pa, pb, acc, per_block;
+  size_t raised, packed, part_s, part_r, p, total;
+};
+
+CePlan ce_plan(int T, int H, int V, bool grad, int sms) {
+  CePlan q{};
+  const int pairs = sms > 1 ? sms / 2 : 74;
+  q.block = std::min(std::max(T, 1), ROW_BLOCK);
+  q.blocks = (std::max(T, 1) + q.block - 1) / q.block;
+  q.tcap = (q.block + TILE - 1) / TILE * TILE;
+  q.tiles = (V + TILE - 1) / TILE;
+  const int mt = q.tcap / TILE;
+  if (grad) {
+    // a piece's tiles fill whole waves of CTA pairs, as many as P's bytes allow
+    const long long most = std::max(1ll, P_BYTES / (static_cast<long long>(q.tcap) * TILE * 2));
+    long long n = std::min<long long>(most, q.tiles);
+    const long long waves = n * mt / pairs;
+    if (waves >= 1 && n < q.tiles) n = waves * pairs / mt;
+    q.piece_tiles = static_cast<int>(std::max(1ll, n));
+    // K ranges of the gradient's tiles: the fewest that fill the last wave of pairs
+    const int units = mt * ((H + TILE - 1) / TILE);
+    double best = 1e30;
+    q.splits = 1;
+    const int kb = (std::min(V, q.piece_tiles * TILE) + BK - 1) / BK;  // of the first piece: no range is empty in it
+    for (int s = 1; s <= std::min(MAX_SPLITS, kb); ++s) {
+      const double cost = static_cast<double>((units * s + pairs - 1) / pairs) / s * (1.0 + 0.02 * s);
+      if (cost < best) {
+        best = cost;
+        q.splits = s;
+      }
+    }
+  } else {
+    q.piece_tiles = q.tiles;
+    q.splits = 0;
+  }
+  q.pieces = (q.tiles + q.piece_tiles - 1) / q.piece_tiles;
+  size_t o = 0;
+  const size_t rows = static_cast<size_t>(q.tcap);
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += up256(bytes);
+    return at;
+  };
+  q.n_rows = take(4);
+  q.place = take(rows * 4);
+  q.target = take(rows * 8);
+  q.row = take(rows * 4);
+  q.ref = take(rows * 4);
+  q.la = take(rows * 4);
+  q.lb = take(rows * 4);
+  q.inv_z = take(rows * 4);
+  q.pa = take(rows * 8);
+  q.pb = take(rows * 8);
+  q.acc = take(static_cast<size_t>(q.splits) * rows * H * 4);
+  q.per_block = o;
+  o *= q.blocks;
+  q.raised = take(static_cast<size_t>(q.pieces) * 4);
+  q.packed = take(rows * H * 2);
+  q.part_s = take(static_cast<size_t>(q.tiles) * rows * 4);
+  q.part_r = take(static_cast<size_t>(q.tiles) * rows * 4);
+  q.p = take(grad ? rows * q.piece_tiles * TILE * 2 : 0);
+  q.total = o;
+  return q;
+}
+
+CeRows rows_of(const CePlan& q, uint8_t* b) {
+  return CeRows{reinterpret_cast<int2*>(b + q.target), reinterpret_cast<int*>(b + q.row),
+                reinterpret_cast<float*>(b + q.ref),   reinterpret_cast<float*>(b + q.la),
+                reinterpret_cast<float*>(b + q.lb),    reinterpret_cast<float*>(b + q.inv_z),
+                reinterpret_cast<float2*>(b + q.pa),   reinterpret_cast<float2*>(b + q.pb)};
+}
+
+int row_threads(int h) { return std::max(32, std::min(512, (h / 8 + 31) / 32 * 32)); }
+
+#define CE_CK(call)                       \
+  do {                                    \
+    const cudaError_t e_ = (call);        \
+    if (e_ != cudaSuccess) return e_;     \
+  } while (0)
+
+cudaError_t gemm_attributes() {
+  // per device and cheap, so set before each call: two function attributes
+  CE_CK(cudaFuncSetAttribute(ce_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
+  return cudaFuncSetAttribute(ce_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+}
+
+}  // namespace
+
+size_t linear_ce_workspace(int T, int H, int V, bool grad) { return ce_plan(T, H, V, grad, device_sm_count()).total; }
+
+cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_t* w, long long ldw, int T, int H, int V,
+                                 const int32_t* t1, const int32_t* t2, bool grad, float* lse, float* logp, float* logp2,
+                                 uint8_t* ws, int* err, cudaStream_t st) {
+  const int sms = device_sm_count();
+  const CePlan q = ce_plan(T, H, V, grad, sms);
+  CE_CK(gemm_attributes());
+  int* raised = reinterpret_cast<int*>(ws + q.raised);
+  uint16_t* packed = reinterpret_cast<uint16_t*>(ws + q.packed);
+  float* part_s = reinterpret_cast<float*>(ws + q.part_s);
+  float* part_r = reinterpret_cast<float*>(ws + q.part_r);
+  uint16_t* P = reinterpret_cast<uint16_t*>(ws + q.p);
+  const long long ldp = static_cast<long long>(q.piece_tiles) * TILE;
+  CeGemm a{}, b{};
+  if (!tma_encode_sw128(&a.ta, packed, false, H, q.tcap, 2ull * H, BK, 128) ||
+      !tma_encode_sw128(&a.tb, w, false, H, V, 2ull * ldw, BK, 128) ||
+      (grad && (!tma_encode_sw128(&a.to, P, false, ldp, q.tcap, 2ull * ldp, BK, 128) ||
+                !tma_encode_sw128(&b.tb, w, false, H, V, 2ull * ldw, 64, BK))))
+    return cudaErrorInvalidValue;
+  b.ta = a.to;
+  a.kb = (H + BK - 1) / BK;
+  a.tcap = b.tcap = q.tcap;
+  a.part_s = part_s;
+  a.part_r = part_r;
+  a.store_p = grad;
+  a.err = b.err = err;
+  b.n_tiles = (H + TILE - 1) / TILE;
+  b.splits = q.splits;
+  b.cols = H;
+  const dim3 grid(2 * std::max(1, sms / 2));
+  for (int k = 0; k < q.blocks; ++k) {
+    const int t0 = k * q.block, n = std::min(q.block, T - t0);
+    uint8_t* base = ws + k * q.per_block;
+    const CeRows rows = rows_of(q, base);
+    int* n_rows = reinterpret_cast<int*>(base + q.n_rows);
+    float* acc = reinterpret_cast<float*>(base + q.acc);
+    ce_prepare_kernel<<<n, row_threads(H), 0, st>>>(h + t0 * ldh, ldh, w, ldw, n, H, V, t1 + t0, t2 ? t2 + t0 : nullptr,
+                                                    packed, rows, reinterpret_cast<int*>(base + q.place), n_rows, raised,
+                                                    q.pieces, lse ? lse + t0 : nullptr, logp + t0,
+                                                    logp2 ? logp2 + t0 : nullptr, err);
+    CE_CK(cudaGetLastError());
+    ++g_kernel_launches;
+    if (grad && !tma_encode_sw128(&b.to, acc, true, H, static_cast<unsigned long long>(q.splits) * q.tcap, 4ull * H, 32, 128))
+      return cudaErrorInvalidValue;
+    a.n_rows = b.n_rows = n_rows;
+    a.target = rows.target;
+    a.ref = rows.ref;
+    for (int i = 0; i < q.pieces; ++i) {
+      a.tile0 = i * q.piece_tiles;
+      a.n_tiles = std::min(q.piece_tiles, q.tiles - a.tile0);
+      a.w_row0 = b.w_row0 = a.tile0 * TILE;
+      a.cols = std::min(V - a.w_row0, a.n_tiles * TILE);
+      a.raised = raised + i;
+      ce_gemm_kernel<false><<<grid, THREADS, SMEM_BYTES, st>>>(a);
+      CE_CK(cudaGetLastError());
+      ++g_kernel_launches;
+      if (!grad) continue;
+      ce_raise_kernel<<<64, 256, 0, st>>>(raised + i, n_rows, a.tile0, a.n_tiles, q.tcap, part_r, rows.ref, P, ldp, acc,
+                                          q.splits, H, i > 0);
+      CE_CK(cudaGetLastError());
+      b.kb = (a.cols + BK - 1) / BK;
+      b.accumulate = i > 0;
+      ce_gemm_kernel<true><<<grid, THREADS, SMEM_BYTES, st>>>(b);
+      CE_CK(cudaGetLastError());
+      g_kernel_launches += 2;
+    }
+    ce_stats_kernel<<<(n + 31) / 32, 256, 0, st>>>(n_rows, q.tiles, q.tcap, part_s, part_r, rows, lse ? lse + t0 : nullptr,
+                                                   logp + t0, logp2 ? logp2 + t0 : nullptr);
+    CE_CK(cudaGetLastError());
+    ++g_kernel_launches;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t linear_ce_bwd_launch(const uint16_t* w, long long ldw, int T, int H, int V, const float* weight,
+                                 const float* weight2, uint16_t* dh, long long ldd, uint8_t* ws, cudaStream_t st) {
+  const CePlan q = ce_plan(T, H, V, true, device_sm_count());
+  for (int k = 0; k < q.blocks; ++k) {
+    const int t0 = k * q.block, n = std::min(q.block, T - t0);
+    uint8_t* base = ws + k * q.per_block;
+    ce_dh_kernel<<<n, row_threads(H), 0, st>>>(reinterpret_cast<int*>(base + q.place), rows_of(q, base), weight + t0,
+                                               weight2 ? weight2 + t0 : nullptr, reinterpret_cast<float*>(base + q.acc),
+                                               q.splits, q.tcap, w, ldw, H, dh + t0 * ldd, ldd);
+    CE_CK(cudaGetLastError());
+    ++g_kernel_launches;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace soup

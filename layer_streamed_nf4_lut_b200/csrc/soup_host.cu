@@ -2166,6 +2166,152 @@ soup_status soup_nf4_matmul(const void* x, int M, int N, int K, const uint8_t* c
   return e == cudaSuccess ? SOUP_OK : SOUP_ERR_CUDA;
 }
 
+
+// ---- loss in pieces of the vocabulary, AdamW over many tensors, rotary positions
+namespace {
+bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+soup_status of_launch(cudaError_t e) {
+  if (e == cudaSuccess) return SOUP_OK;
+  return e == cudaErrorInvalidValue ? SOUP_ERR_INVALID_ARG : SOUP_ERR_CUDA;
+}
+soup_status linear_ce_sizes(int T, int hidden, int vocab) {
+  if (T < 0 || hidden < 1 || vocab < 1) return SOUP_ERR_INVALID_ARG;
+  return (hidden % 8 || T >= (1 << 24) || hidden > (1 << 16) || vocab > (1 << 22)) ? SOUP_ERR_UNSUPPORTED : SOUP_OK;
+}
+}  // namespace
+
+soup_status soup_linear_ce_workspace(int T, int hidden, int vocab, int grad, size_t* bytes) {
+  if (!bytes) return SOUP_ERR_INVALID_ARG;
+  SOUP_TRY(linear_ce_sizes(T, hidden, vocab));
+  *bytes = linear_ce_workspace(T, hidden, vocab, grad != 0);
+  return SOUP_OK;
+}
+
+soup_status soup_linear_ce_fwd(const void* h, long long ldh, const void* w, long long ldw, int T, int hidden, int vocab,
+                               const int32_t* t1, const int32_t* t2, int grad, float* lse, float* logp, float* logp2,
+                               void* ws, size_t ws_bytes, int* err, void* stream) {
+  SOUP_TRY(linear_ce_sizes(T, hidden, vocab));
+  if (T == 0) return SOUP_OK;
+  if (!h || !w || !t1 || !logp || !ws || (t2 && !logp2)) return SOUP_ERR_INVALID_ARG;
+  if (ldh < hidden || ldw < hidden || ldh % 8 || ldw % 8) return SOUP_ERR_INVALID_ARG;
+  if (misaligned(h, 16) || misaligned(w, 16) || misaligned(ws, 256) || misaligned(t1, 4) || misaligned(t2, 4) ||
+      misaligned(lse, 4) || misaligned(logp, 4) || misaligned(logp2, 4))
+    return SOUP_ERR_INVALID_ARG;
+  if (ws_bytes < linear_ce_workspace(T, hidden, vocab, grad != 0)) return SOUP_ERR_INVALID_ARG;
+  return of_launch(linear_ce_fwd_launch(static_cast<const uint16_t*>(h), ldh, static_cast<const uint16_t*>(w), ldw, T,
+                                        hidden, vocab, t1, t2, grad != 0, lse, logp, t2 ? logp2 : nullptr,
+                                        static_cast<uint8_t*>(ws), err, static_cast<cudaStream_t>(stream)));
+}
+
+soup_status soup_linear_ce_bwd(const void* w, long long ldw, int T, int hidden, int vocab, const float* weight,
+                               const float* weight2, void* dh, long long ldd, void* ws, size_t ws_bytes, void* stream) {
+  SOUP_TRY(linear_ce_sizes(T, hidden, vocab));
+  if (T == 0) return SOUP_OK;
+  if (!w || !weight || !dh || !ws) return SOUP_ERR_INVALID_ARG;
+  if (ldw < hidden || ldd < hidden || ldw % 8 || ldd % 8) return SOUP_ERR_INVALID_ARG;
+  if (misaligned(w, 16) || misaligned(dh, 16) || misaligned(ws, 256) || misaligned(weight, 4) || misaligned(weight2, 4))
+    return SOUP_ERR_INVALID_ARG;
+  if (ws_bytes < linear_ce_workspace(T, hidden, vocab, true)) return SOUP_ERR_INVALID_ARG;
+  return of_launch(linear_ce_bwd_launch(static_cast<const uint16_t*>(w), ldw, T, hidden, vocab, weight, weight2,
+                                        static_cast<uint16_t*>(dh), ldd, static_cast<uint8_t*>(ws),
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+soup_status soup_adamw_state_numel(const soup_adamw_tensor* tensors, int count, long long* numel) {
+  if (!numel || count < 0 || (count && !tensors)) return SOUP_ERR_INVALID_ARG;
+  long long n = 0;
+  for (int i = 0; i < count; ++i) {
+    if (tensors[i].n < 0) return SOUP_ERR_INVALID_ARG;
+    n += (tensors[i].n + ADAMW_BLOCK - 1) / ADAMW_BLOCK * ADAMW_BLOCK;
+  }
+  *numel = n;
+  return SOUP_OK;
+}
+
+soup_status soup_adamw_multi(const soup_adamw_tensor* tensors, int count, const soup_adamw_options* o, void* m, void* v,
+                             float* m_scale, float* v_scale, const float* hp, void* stream) {
+  if (count < 0 || (count && !tensors) || !o) return SOUP_ERR_INVALID_ARG;
+  if ((m_scale == nullptr) != (v_scale == nullptr) || (!hp && o->step < 1)) return SOUP_ERR_INVALID_ARG;
+  const unsigned ps = o->params_bf16 ? 2 : 4, gs = o->grads_bf16 ? 2 : 4;
+  bool any = false;
+  for (int i = 0; i < count; ++i) {
+    const soup_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return SOUP_ERR_INVALID_ARG;
+    if (t.n == 0) continue;
+    any = true;
+    if (!t.p || !t.g || misaligned(t.p, ps) || misaligned(t.g, gs) || misaligned(t.p_bf16_copy, 2))
+      return SOUP_ERR_INVALID_ARG;
+  }
+  if (!any) return SOUP_OK;
+  if (!m || !v || misaligned(m, 16) || misaligned(v, 16) || misaligned(m_scale, 4) || misaligned(v_scale, 4) ||
+      misaligned(hp, 4))
+    return SOUP_ERR_INVALID_ARG;
+  return of_launch(adamw_multi_launch(tensors, count, *o, m, v, m_scale, v_scale, hp, static_cast<cudaStream_t>(stream)));
+}
+
+soup_status soup_adamw_state_values(const void* m, const void* v, const float* m_scale, const float* v_scale, long long n,
+                                    uint16_t* m_out, uint16_t* v_out, void* stream) {
+  if (n < 0 || n % ADAMW_BLOCK) return SOUP_ERR_INVALID_ARG;
+  if (n == 0) return SOUP_OK;
+  if (!m || !v || !m_scale || !v_scale || !m_out || !v_out || misaligned(m, 8) || misaligned(v, 8) ||
+      misaligned(m_out, 16) || misaligned(v_out, 16) || misaligned(m_scale, 4) || misaligned(v_scale, 4))
+    return SOUP_ERR_INVALID_ARG;
+  return of_launch(adamw_values_launch(static_cast<const uint8_t*>(m), static_cast<const uint8_t*>(v), m_scale, v_scale,
+                                       n, m_out, v_out, static_cast<cudaStream_t>(stream)));
+}
+
+static soup_status rope_check(const soup_rope_config* cfg) {
+  std::string why;
+  if (!cfg || !rope_config_ok(*cfg, why)) return SOUP_ERR_INVALID_ARG;
+  return (cfg->rotary_dim % 2 || cfg->rotary_dim > 2 * ROPE_MAX_PAIRS) ? SOUP_ERR_UNSUPPORTED : SOUP_OK;
+}
+
+soup_status soup_rope_frequencies(const soup_rope_config* cfg, double* freq, double* factor_on_cos_sin) {
+  if (!freq || !factor_on_cos_sin) return SOUP_ERR_INVALID_ARG;
+  SOUP_TRY(rope_check(cfg));
+  rope_frequencies(*cfg, freq, factor_on_cos_sin);
+  return SOUP_OK;
+}
+
+soup_status soup_rope(const soup_rope_config* cfg, const void* q, long long ldq, void* q_out, long long ldq_out, int heads_q,
+                      const void* k, long long ldk, void* k_out, long long ldk_out, int heads_k, int head_dim, int T,
+                      const int32_t* positions, int dtype, int inverse, void* stream) {
+  SOUP_TRY(rope_check(cfg));
+  if (T < 0 || heads_q < 0 || heads_k < 0 || head_dim < 1 || dtype < 0 || dtype > 1) return SOUP_ERR_INVALID_ARG;
+  if (cfg->rotary_dim > head_dim) return SOUP_ERR_UNSUPPORTED;
+  if (T == 0 || heads_q + heads_k == 0) return SOUP_OK;
+  if (!positions || misaligned(positions, 4)) return SOUP_ERR_INVALID_ARG;
+  RopeCall c{};
+  const void* x[2] = {q, k};
+  void* y[2] = {q_out, k_out};
+  const long long ldx[2] = {ldq, ldk}, ldy[2] = {ldq_out, ldk_out};
+  const int heads[2] = {heads_q, heads_k};
+  for (int i = 0; i < 2; ++i) {
+    if (!heads[i]) continue;
+    const long long row = static_cast<long long>(heads[i]) * head_dim;
+    if (!x[i] || !y[i] || misaligned(x[i], dtype ? 4 : 2) || misaligned(y[i], dtype ? 4 : 2) || row > INT_MAX ||
+        (T > 1 && (ldx[i] < row || ldy[i] < row)) || (x[i] == y[i] && ldx[i] != ldy[i]))
+      return SOUP_ERR_INVALID_ARG;
+    c.x[i] = x[i];
+    c.y[i] = y[i];
+    c.ldx[i] = ldx[i];
+    c.ldy[i] = ldy[i];
+    c.heads[i] = heads[i];
+  }
+  double freq[ROPE_MAX_PAIRS], grow;
+  rope_frequencies(*cfg, freq, &grow);
+  c.head_dim = head_dim;
+  c.rotary = cfg->rotary_dim;
+  c.T = T;
+  c.f32 = dtype;
+  c.interleaved = cfg->interleaved != 0;
+  c.back = inverse != 0;
+  c.positions = positions;
+  c.grow = static_cast<float>(grow);
+  c.freq = freq;
+  return of_launch(rope_launch(c, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"
 
 // The library's NF4 levels for other translation units.

@@ -1,0 +1,432 @@
+"""The loss in pieces of the vocabulary, AdamW over many tensors and rotary positions, each against its
+formula in float64 (torch on the GPU, elementary operations), with tolerances from the roundings
+the kernels make."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16 = 2.0 ** -8  # one rounding to bf16, relative to the value
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# ------------------------------------------------------------------ loss
+def ce_reference(h, w, t1, weight=None, t2=None, weight2=None):
+    """lse, logp, logp2, dh in float64, and the bounds of the kernels' errors: of a logit (and so of
+    logp and lse), and of each element of dh."""
+    h, w = h.double(), w.double()
+    V = w.shape[0]
+    logits = h @ w.T
+    size = h.abs() @ w.abs().T
+    live = t1 >= 0
+    t1, t2 = t1.long(), (t2.long() if t2 is not None else torch.full_like(t1, -1).long())
+    t2 = torch.where(live, t2, -1)
+    lse = torch.logsumexp(logits, 1)
+    at = lambda t: torch.where(t >= 0, logits.gather(1, t.clamp(min=0)[:, None])[:, 0] - lse, 0.0)
+    out = dict(lse=torch.where(live, lse, 0.0), logp=at(torch.where(live, t1, -1)), logp2=at(t2))
+    # fp32 accumulation of H products, 16 a tensor-core instruction (truncating at worst: 2^-23 each),
+    # the product with log2 e (2^-23 of the logit) and ex2.approx (2^-22)
+    H = h.shape[1]
+    tol = ((H / 16 + 16) * 2.0 ** -23 * size).amax(1) + 2.0 ** -21 * (1 + logits.abs().amax(1) + lse.abs())
+    out["tol"] = tol
+    if weight is not None:
+        p = torch.softmax(logits, 1)
+        w1 = torch.where(live, weight.double(), 0.0)
+        w2 = torch.where(t2 >= 0, weight2.double(), 0.0) if weight2 is not None else torch.zeros_like(w1)
+        col = torch.arange(V, device=h.device)
+        a, b = (col == t1[:, None]) & live[:, None], col == t2[:, None]
+        d = p * (w1 + w2)[:, None] - w1[:, None] * a - w2[:, None] * b
+        out["dh"] = d @ w
+        # P is rounded to bf16 once, p is off by e^(2 tol) - 1 at most; one more rounding of the result
+        each = BF16 + 4 * tol[:, None] + 2.0 ** -12
+        out["dh_tol"] = each * (d.abs() @ w.abs()) + BF16 * out["dh"].abs() + 1e-38
+    return out
+
+
+def check_ce(h, w, t1, weight=None, t2=None, weight2=None):
+    from layer_streamed_nf4_lut_b200 import model as M
+    got = M.linear_ce(h, w, t1, weight, t2, weight2, check_targets=True)
+    want = ce_reference(h, w, t1, weight, t2, weight2)
+    for k in ("lse", "logp") + (("logp2",) if t2 is not None else ()):
+        assert torch.isfinite(got[k]).all(), k
+        worst = ((got[k].double() - want[k]).abs() - want["tol"]).max().item()
+        assert worst <= 0, (k, worst)
+    if weight is not None:
+        worst = ((got["dh"].double() - want["dh"]).abs() - want["dh_tol"]).max().item()
+        assert worst <= 0, ("dh", worst)
+        dead = (t1 < 0)
+        assert (got["dh"][dead] == 0).all()
+    assert (got["logp"][t1 < 0] == 0).all() and (got["lse"][t1 < 0] == 0).all()
+    return got
+
+
+def ce_inputs(T, H, V, seed, counted=1.0, sure=True):
+    g = gen(seed)
+    w = (torch.randn(V, H, generator=g, device="cuda") * 0.02).bfloat16()
+    t1 = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    h = torch.randn(T, H, generator=g, device="cuda")
+    if sure:
+        h = h + torch.rand(T, 1, generator=g, device="cuda") * (20 / (H * 0.0004)) * w[t1.long()].float()
+    t1 = torch.where(torch.rand(T, generator=g, device="cuda") < counted, t1, -1).int()
+    return h.bfloat16(), w, t1, torch.randn(T, generator=g, device="cuda") * 0.01
+
+
+@pytest.mark.parametrize("T,H,V", [(1, 8, 1), (1, 64, 2), (2, 8, 5), (1, 4096, 1000), (64, 256, 1024), (63, 200, 255),
+                                   (65, 72, 256), (257, 136, 257), (300, 1032, 1000), (512, 512, 4099), (1000, 264, 3001)])
+@pytest.mark.parametrize("counted", [1.0, 0.4])
+def test_loss_and_gradient(T, H, V, counted):
+    h, w, t1, weight = ce_inputs(T, H, V, T + H + V, counted)
+    check_ce(h, w, t1, weight)
+    check_ce(h, w, t1)  # without a gradient
+
+
+def test_several_pieces_and_blocks_of_rows():
+    # 4096 rows take pieces of the vocabulary; rows past them a second walk over it
+    h, w, t1, weight = ce_inputs(4096, 64, 21000, 3)
+    check_ce(h, w, t1, weight)
+    h, w, t1, weight = ce_inputs(4500, 40, 700, 4, 0.7)
+    check_ce(h, w, t1, weight)
+
+
+def test_no_row_has_a_target():
+    h, w, t1, weight = ce_inputs(70, 64, 300, 5)
+    check_ce(h, w, torch.full_like(t1, -1), weight)
+    t1 = torch.full_like(t1, -1)
+    t1[69] = 299  # the last row alone, its target the last column
+    check_ce(h, w, t1, weight)
+
+
+def test_no_rows():
+    from layer_streamed_nf4_lut_b200 import model as M
+    h, w, t1, weight = ce_inputs(4, 64, 300, 6)
+    got = M.linear_ce(h[:0], w, t1[:0], weight[:0])
+    assert got["logp"].shape == (0,) and got["dh"].shape == (0, 64)
+
+
+@pytest.mark.parametrize("T,H,V", [(9, 64, 300), (200, 128, 2050)])
+def test_two_targets(T, H, V):
+    h, w, t1, weight = ce_inputs(T, H, V, 7, 0.8)
+    g = gen(8)
+    t2 = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    t2 = torch.where(torch.rand(T, generator=g, device="cuda") < 0.5, t2, -1).int()
+    t2[:4] = t1[:4]  # the same target twice
+    check_ce(h, w, t1, weight, t2, -0.7 * weight.flip(0).contiguous())
+
+
+def test_rows_and_weights_with_strides():
+    h, w, t1, weight = ce_inputs(100, 64, 500, 9)
+    hs = torch.full((100, 96), float("nan"), device="cuda", dtype=torch.bfloat16)
+    ws = torch.full((500, 72), float("nan"), device="cuda", dtype=torch.bfloat16)
+    hs[:, 16:80] = h
+    ws[:, 8:72] = w
+    got = check_ce(hs[:, 16:80], ws[:, 8:72], t1, weight)
+    base = check_ce(h, w, t1, weight)
+    assert all(torch.equal(got[k], base[k]) for k in base)
+
+
+def test_a_certain_row_keeps_a_relative_gradient():
+    """p_y within 1e-6 of 1: the gradient is about 1e-6 of a row of W, and right to bf16's precision."""
+    T, H, V = 32, 256, 700
+    h, w, t1, _ = ce_inputs(T, H, V, 10, sure=False)
+    h = (w[t1.long()].float() * (20.0 / (H * 0.0004))).bfloat16()
+    weight = torch.ones(T, device="cuda")
+    check_ce(h, w, t1, weight)
+
+
+@pytest.mark.parametrize("T,V", [(40, 900), (4096, 17000)])
+def test_logits_far_above_the_target(T, V):
+    """Rows whose other logits exceed the target's by more than an exponential's range, some in a later
+    piece of the vocabulary than others."""
+    H = 64
+    h, w, t1, weight = ce_inputs(T, H, V, 11, sure=False)
+    h[::3] *= 60  # logits of about +-400
+    w[V // 2:] *= 2
+    w[V - 3] *= 4
+    check_ce(h, w, t1, weight)
+
+
+def test_a_row_of_nan_stays_alone():
+    from layer_streamed_nf4_lut_b200 import model as M
+    h, w, t1, weight = ce_inputs(50, 64, 400, 12)
+    base = M.linear_ce(h, w, t1, weight)
+    bad = h.clone()
+    bad[7] = float("nan")
+    bad[20, 3] = float("inf")
+    got = M.linear_ce(bad, w, t1, weight)
+    rest = torch.ones(50, dtype=torch.bool, device="cuda")
+    rest[[7, 20]] = False
+    for k in base:
+        assert torch.equal(got[k][rest], base[k][rest]), k
+        assert not torch.isfinite(got[k][[7, 20]]).all(1 if k == "dh" else 0).any(), k
+
+
+def test_targets_beyond_the_vocabulary_are_reported():
+    from layer_streamed_nf4_lut_b200 import model as M
+    h, w, t1, weight = ce_inputs(20, 64, 400, 13)
+    t1[5] = 400
+    with pytest.raises(M.SoupError) as e:
+        M.linear_ce(h, w, t1, weight, check_targets=True)
+    assert e.value.status == -6
+    got = M.linear_ce(h, w, t1, weight)
+    assert got["logp"][5] == 0 and (got["dh"][5] == 0).all() and torch.isfinite(got["dh"].float()).all()
+
+
+def test_gradient_against_differences():
+    """-sum(weight logp) along a direction: central differences of the library's own log-probs."""
+    from layer_streamed_nf4_lut_b200 import model as M
+    T, H, V = 48, 128, 600
+    h, w, t1, weight = ce_inputs(T, H, V, 14, 0.8)
+    weight = weight.abs() * 100
+    dh = M.linear_ce(h, w, t1, weight)["dh"].double()
+    loss = lambda x: -(weight.double() * M.linear_ce(x, w, t1)["logp"].double()).sum()
+    # a direction of whole bf16 steps, so that h +- d are bf16 values
+    step = 0.25 * torch.sign(torch.randn(T, H, generator=gen(15), device="cuda"))
+    step = torch.where(torch.rand(T, H, generator=gen(16), device="cuda") < 0.05, step, 0.0)
+    up, down = (h.float() + step).bfloat16(), (h.float() - step).bfloat16()
+    moved = (up.double() - down.double())
+    slope = (dh * moved).sum().item()
+    diff = (loss(up) - loss(down)).item()
+    size = (dh * moved).abs().sum().item()
+    # third derivatives of logp are at most max|d l|^3 = (sum |step w|)^3 per row
+    third = ((moved / 2).abs() @ w.double().abs().amax(0)[:, None]).pow(3).squeeze(1)
+    assert abs(slope - diff) <= 2 * BF16 * size + (weight.double() * third).sum().item() + 1e-4
+
+
+def test_same_bits_again_on_other_streams_and_captured():
+    from layer_streamed_nf4_lut_b200 import model as M
+    h, w, t1, weight = ce_inputs(300, 512, 5000, 17, 0.7)
+    h2, w2, t2, weight2 = ce_inputs(200, 256, 3000, 18)
+    a, b = M.linear_ce(h, w, t1, weight), M.linear_ce(h2, w2, t2, weight2)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):  # two calls at once
+        with torch.cuda.stream(s1):
+            c = M.linear_ce(h, w, t1, weight)
+        with torch.cuda.stream(s2):
+            d = M.linear_ce(h2, w2, t2, weight2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[k], c[k]) for k in a) and all(torch.equal(b[k], d[k]) for k in b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        e = M.linear_ce(h, w, t1, weight)
+    for _ in range(2):
+        for k in e:
+            e[k].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[k], e[k]) for k in a)
+
+
+def test_weights_known_after_the_log_probs():
+    from layer_streamed_nf4_lut_b200 import model as M
+    h, w, t1, weight = ce_inputs(130, 256, 900, 19, 0.6)
+    fwd = M.linear_ce_fwd(h, w, t1)
+    late = fwd["logp"].exp().contiguous()
+    dh = M.linear_ce_bwd(w, fwd["saved"], late)
+    assert torch.equal(dh, M.linear_ce(h, w, t1, late)["dh"])
+    # a gradient may be asked for twice
+    assert torch.equal(M.linear_ce_bwd(w, fwd["saved"], weight), M.linear_ce(h, w, t1, weight)["dh"])
+
+
+# ------------------------------------------------------------------ AdamW
+def adam_reference(p, g, m, v, lr, step, wd, b1=0.9, b2=0.999, eps=1e-8):
+    p, g, m, v = (x.double() for x in (p, g, m, v))
+    size = b1 * m.abs() + (1 - b1) * g.abs()  # of the terms of m', which may cancel
+    m = b1 * m + (1 - b1) * g
+    v = b2 * v + (1 - b2) * g * g
+    under = (1 - b1 ** step) * (torch.sqrt(v / (1 - b2 ** step)) + eps)
+    return p - lr * (m / under + wd * p), m, v, lr * (size / under + wd * p.abs())
+
+
+def m_values(q, scale):
+    r = q.double() / 127
+    return r * r.abs() * scale.double().repeat_interleave(256)
+
+
+def v_values(q, scale):
+    return (q.double() / 255) ** 4 * scale.double().repeat_interleave(256)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("pt,gt", [(torch.float32, torch.float32), (torch.float32, torch.bfloat16),
+                                   (torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32)])
+@pytest.mark.parametrize("sizes", [[1], [256], [255, 257, 8, 0, 1, 1000, 4096], [5000] * 700, [3000001]])
+def test_adamw_steps(bits, pt, gt, sizes):
+    from layer_streamed_nf4_lut_b200 import model as M
+    g = gen(sum(sizes) + bits)
+    n = sum(sizes)
+    flat = (torch.randn(n, generator=g, device="cuda") * 0.05).to(pt)
+    params = list(flat.split(sizes))  # views at every alignment
+    state = M.adamw_state(sizes, bits)
+    where = torch.cat([256 * b + torch.arange(k, device="cuda") for b, k in
+                       zip(np.cumsum([0] + [-(-k // 256) for k in sizes])[:-1].tolist(), sizes)])
+    unused = torch.ones(state["m"].numel(), dtype=torch.bool, device="cuda")
+    unused[where] = False
+    for step in (1, 2, 3):
+        grad = (torch.randn(n, generator=g, device="cuda") * torch.exp(2 * torch.randn(n, generator=g, device="cuda")) * 1e-3).to(gt)
+        grad[torch.rand(n, generator=g, device="cuda") < 0.1] = 0
+        before = flat.clone()
+        if bits == 8:
+            m0, v0 = m_values(state["m"], state["m_scale"]), v_values(state["v"], state["v_scale"])
+        else:
+            m0, v0 = state["m"].double(), state["v"].double()
+        pw, mw, vw, move = adam_reference(before, grad, m0[where], v0[where], 1e-2, step, 0.1)
+        M.adamw_multi(params, list(grad.split(sizes)), lr=1e-2, step=step, weight_decay=0.1, **state)
+        # a dozen fp32 roundings (2^-24 each) of the step, relative to the terms of m', which may cancel;
+        # one of the result (bf16: one more)
+        tol = 2.0 ** -20 * move + 2.0 ** -22 * before.double().abs() + (BF16 * pw.abs() if pt == torch.bfloat16 else 0) + 1e-38
+        assert ((flat.double() - pw).abs() <= tol).all()
+        full_m = torch.zeros_like(m0).index_copy_(0, where, mw)
+        full_v = torch.zeros_like(v0).index_copy_(0, where, vw)
+        m_size = torch.zeros_like(m0).index_copy_(0, where, 0.9 * m0[where].abs() + 0.1 * grad.double().abs())
+        if bits == 32:
+            assert ((state["m"].double() - full_m).abs() <= 2.0 ** -22 * m_size).all()
+            assert ((state["v"].double() - full_v).abs() <= 2.0 ** -21 * full_v).all()
+        else:
+            ms, vs = full_m.abs().view(-1, 256).amax(1), full_v.view(-1, 256).amax(1)
+            assert ((state["m_scale"].double() - ms).abs() <= 2.0 ** -21 * m_size.view(-1, 256).amax(1)).all()
+            assert ((state["v_scale"].double() - vs).abs() <= 2.0 ** -21 * vs).all()
+            # a code is the nearest one, up to the roundings of its argument (relative 2^-19, and the
+            # cancellation of m' in units of its block's scale)
+            x = 127 * (full_m.abs() / ms.clamp(min=1e-300).repeat_interleave(256)).sqrt()
+            slip = 127 * ((2.0 ** -22 * m_size) / ms.clamp(min=1e-300).repeat_interleave(256)).sqrt()
+            off = (state["m"].double().abs() - x).abs()
+            assert (off <= 0.5 + 127 * 2.0 ** -19 + slip).all()
+            assert (torch.sign(state["m"].double()) * torch.sign(full_m) >= 0).all()
+            y = 255 * (full_v / vs.clamp(min=1e-300).repeat_interleave(256)) ** 0.25
+            wanted = torch.where(full_v > 0, y.clamp(min=1), y)
+            assert ((state["v"].double() - wanted).abs() <= 0.5 + 255 * 2.0 ** -19).all()
+            assert (state["v"][full_v > 0] > 0).all()
+        assert (state["m"][unused] == 0).all() and (state["v"][unused] == 0).all()
+    if bits == 8:
+        mo, vo = M.adamw_state_values(**state)
+        mv, vv = m_values(state["m"], state["m_scale"]), v_values(state["v"], state["v_scale"])
+        assert ((mo.double() - mv).abs() <= (BF16 + 2.0 ** -20) * mv.abs() + 1e-38).all()
+        assert ((vo.double() - vv).abs() <= (BF16 + 2.0 ** -20) * vv.abs() + 1e-38).all()
+
+
+def test_adamw_tiny_gradients_and_nan():
+    from layer_streamed_nf4_lut_b200 import model as M
+    p = torch.zeros(1024, device="cuda")
+    g = torch.full((1024,), 1e-18, device="cuda")  # g^2 is below fp32's normal range
+    g[256:512] = 0
+    g[600] = float("nan")
+    state = M.adamw_state([1024], 8)
+    M.adamw_multi([p], [g], lr=1.0, step=1, **state)
+    assert (state["m"][:256] == 127).all() and (p[:256] < 0).all()
+    assert (state["m"][256:512] == 0).all() and (p[256:512] == 0).all()
+    m, v = M.adamw_state_values(**state)
+    assert torch.isnan(m[512:768]).all() and torch.isnan(v[512:768]).all() and torch.isnan(p[600])  # seen, not hidden
+    assert torch.isfinite(m[768:]).all() and torch.isfinite(p[768:]).all() and torch.isfinite(p[512:600]).all()
+
+
+def test_adamw_device_hyper_parameters_in_a_graph():
+    from layer_streamed_nf4_lut_b200 import model as M
+    sizes = [300, 5000, 64]
+    start = torch.randn(sum(sizes), generator=gen(1), device="cuda")
+    grad = torch.randn(sum(sizes), generator=gen(2), device="cuda")
+    a, b = start.clone(), start.clone()
+    sa, sb = M.adamw_state(sizes, 8), M.adamw_state(sizes, 8)
+    hp = torch.zeros(3, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.adamw_multi(list(a.split(sizes)), list(grad.split(sizes)), lr=0.0, step=1, hp=hp, **sa)
+    for step in (1, 2, 3):
+        lr = 1e-2 / step
+        hp.copy_(torch.tensor([lr, 1 / (1 - 0.9 ** step), 1 / (1 - 0.999 ** step)]))
+        graph.replay()
+        M.adamw_multi(list(b.split(sizes)), list(grad.split(sizes)), lr=lr, step=step, **sb)
+        assert torch.equal(a, b) and all(torch.equal(sa[k], sb[k]) for k in sa)
+
+
+def test_adamw_8_bit_states_follow_32_bit_ones():
+    """Ten steps on noisy gradients of one direction: coded states move the parameters as the uncoded
+    ones do, to the codes' precision (a half step is 1 / 254 of sqrt(|m| / scale))."""
+    from layer_streamed_nf4_lut_b200 import model as M
+    n = 1 << 16
+    a, b = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    sa, sb = M.adamw_state([n], 8), M.adamw_state([n], 32)
+    base = torch.randn(n, generator=gen(3), device="cuda")
+    for step in range(1, 11):
+        grad = base + 0.1 * torch.randn(n, generator=gen(10 + step), device="cuda")
+        M.adamw_multi([a], [grad], lr=1e-2, step=step, **sa)
+        M.adamw_multi([b], [grad], lr=1e-2, step=step, **sb)
+    rel = ((a - b).norm() / b.norm()).item()
+    assert rel < 10 * 2 / 254, rel
+
+
+# ------------------------------------------------------------------ rotary positions
+def rope_reference(x, pos, freq, grow, rotary, interleaved, inverse):
+    x = x.double()
+    ang = pos.double()[:, None] * torch.from_numpy(freq).to(x.device)
+    if inverse:
+        ang = -ang
+    c, s = (grow * torch.cos(ang))[:, None], (grow * torch.sin(ang))[:, None]
+    out = x.clone()
+    i = torch.arange(rotary // 2, device=x.device)
+    ia, ib = (2 * i, 2 * i + 1) if interleaved else (i, i + rotary // 2)
+    out[..., ia] = x[..., ia] * c - x[..., ib] * s
+    out[..., ib] = x[..., ib] * c + x[..., ia] * s
+    size = x.abs().clone()
+    size[..., ia] = size[..., ib] = (x[..., ia].abs() + x[..., ib].abs()) * grow
+    return out, size
+
+
+@pytest.mark.parametrize("T", [1, 7, 300])
+@pytest.mark.parametrize("hq,hkv,d,rotary", [(4, 2, 64, 64), (3, 1, 128, 128), (8, 8, 128, 32), (1, 1, 256, 256), (5, 1, 96, 40),
+                                             (2, 2, 30, 14), (2, 1, 16, 2)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scaling,inverse", [("none", False), ("llama3", True)])
+def test_rope(T, hq, hkv, d, rotary, interleaved, dtype, scaling, inverse):
+    from layer_streamed_nf4_lut_b200 import model as M
+    g = gen(T + d + rotary)
+    packed = torch.randn(T, hq + 2 * hkv, d, generator=g, device="cuda").to(dtype)
+    q, k = packed[:, :hq], packed[:, hq:hq + hkv]
+    pos = torch.randint(0, 1 << 21, (T,), generator=g, device="cuda", dtype=torch.int32)
+    kw = dict(theta=500000.0, rotary_dim=rotary, interleaved=interleaved, scaling=scaling, factor=8.0)
+    freq, grow = M.rope_frequencies(M.rope_config(**kw))
+    qo, ko = M.rope(q, k, pos, inverse=inverse, **kw)
+    half = BF16 if dtype == torch.bfloat16 else 0.0
+    for x, y in ((q, qo), (k, ko)):
+        want, size = rope_reference(x, pos, freq, grow, rotary, interleaved, inverse)
+        # turns are reduced in 64 bits and cos / sin good to 2^-22; one rounding of the result
+        assert ((y.double() - want).abs() <= 2.0 ** -21 * size + half * want.abs()).all()
+        assert torch.equal(y[..., rotary:], x[..., rotary:])
+    v = packed[:, hq + hkv:].clone()
+    M.rope(q, k, pos, inverse=inverse, inplace=True, **kw)
+    assert torch.equal(q, qo) and torch.equal(k, ko) and torch.equal(packed[:, hq + hkv:], v)
+
+
+@pytest.mark.parametrize("scaling", ["none", "linear", "ntk", "llama3", "yarn"])
+def test_rope_back_is_the_gradient(scaling):
+    """<rope(x), y> = <x, rope_back(y)>, far out."""
+    from layer_streamed_nf4_lut_b200 import model as M
+    g = gen(5)
+    x, y = (torch.randn(50, 6, 128, generator=g, device="cuda") for _ in range(2))
+    pos = torch.randint(-100, 1 << 20, (50,), generator=g, device="cuda", dtype=torch.int32)
+    kw = dict(theta=500000.0, rotary_dim=96, scaling=scaling, factor=4.0)
+    a = (M.rope(x, None, pos, **kw)[0].double() * y.double()).sum().item()
+    b = (x.double() * M.rope(y, None, pos, inverse=True, **kw)[0].double()).sum().item()
+    assert abs(a - b) <= 2.0 ** -20 * (x.double().abs() * y.double().abs()).sum().item() * 4
+
+
+def test_rope_rows_past_32_bits_of_offset():
+    """Rows whose place in memory needs more than 32 bits: a packed buffer of 2.2e9 elements."""
+    from layer_streamed_nf4_lut_b200 import model as M
+    T, wide = 1100, 2_000_000
+    buf = torch.zeros(T * wide, dtype=torch.bfloat16, device="cuda")
+    q = buf.as_strided((T, 2, 128), (wide, 128, 1))
+    q.copy_(torch.randn(T, 2, 128, generator=gen(6), device="cuda"))
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    a, _ = M.rope(q, None, pos)
+    b, _ = M.rope(q.contiguous(), None, pos)
+    assert torch.equal(a, b)
+    M.rope(q, None, pos, inplace=True)
+    assert torch.equal(q, b) and int((buf[256:wide] != 0).sum()) == 0

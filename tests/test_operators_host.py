@@ -1,0 +1,190 @@
+"""The loss in pieces of the vocabulary, AdamW over many tensors and rotary positions, as far as no GPU
+is needed: struct layouts, sizes, frequencies and every refusal (refused calls touch nothing, so the
+addresses given here are never read)."""
+import ctypes
+import math
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+from layer_streamed_nf4_lut_b200 import _lib, model as M
+
+L = _lib.lib
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+A = 1 << 20  # an aligned address that no refused call reads
+OK, INVALID, UNSUPPORTED = 0, -1, -7
+
+
+def test_struct_layouts(tmp_path):
+    if shutil.which("gcc") is None:
+        pytest.skip("no C compiler")
+    structs = {"soup_adamw_tensor": _lib.AdamwTensor, "soup_adamw_options": _lib.AdamwOptions,
+               "soup_rope_config": _lib.RopeConfig}
+    lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "soup.h"', "int main(void) {",
+             '  printf("SOUP_ADAMW_BLOCK is %d\\n", SOUP_ADAMW_BLOCK);']
+    for c, cls in structs.items():
+        lines.append(f'  printf("{c} sizeof %zu\\n", sizeof({c}));')
+        lines += [f'  printf("{c} {f} %zu\\n", offsetof({c}, {f}));' for f, _ in cls._fields_]
+    (tmp_path / "a.c").write_text("\n".join(lines + ["  return 0;", "}"]) + "\n")
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(ROOT, "include"), str(tmp_path / "a.c"), "-o", str(tmp_path / "a")],
+                   check=True)
+    got = {tuple(x.split()[:2]): int(x.split()[2]) for x in
+           subprocess.run([str(tmp_path / "a")], check=True, capture_output=True, text=True).stdout.splitlines()}
+    assert got[("SOUP_ADAMW_BLOCK", "is")] == _lib.ADAMW_BLOCK
+    for c, cls in structs.items():
+        assert got[(c, "sizeof")] == ctypes.sizeof(cls)
+        for f, _ in cls._fields_:
+            assert got[(c, f)] == getattr(cls, f).offset, (c, f)
+
+
+# ------------------------------------------------------------------ loss
+def workspace(T, H, V, grad):
+    n = ctypes.c_size_t()
+    assert L.soup_linear_ce_workspace(T, H, V, grad, ctypes.byref(n)) == OK
+    return n.value
+
+
+def test_loss_workspace_is_far_below_the_logits():
+    # fp32 logits and bf16 dlogits of the 8B shape at 2048 tokens are 1.6 GB
+    assert workspace(2048, 4096, 128256, 1) < 0.2 * 2048 * 128256 * 6
+    assert workspace(2048, 4096, 128256, 0) < 0.02 * 2048 * 128256 * 6
+    # and the share that grows with the vocabulary is a few bytes a row and 256 columns
+    assert workspace(4096, 64, 1 << 20, 1) - workspace(4096, 64, 1 << 19, 1) < 4096 * (1 << 19) * 8 / 250 + 8192
+    assert workspace(0, 64, 100, 1) > 0
+
+
+def ce(**kw):
+    a = dict(h=A, ldh=64, w=A, ldw=64, T=4, H=64, V=100, t1=A, t2=None, grad=1, lse=A, logp=A, logp2=None, ws=A,
+             ws_bytes=1 << 40, err=None)
+    a.update(kw)
+    return L.soup_linear_ce_fwd(a["h"], a["ldh"], a["w"], a["ldw"], a["T"], a["H"], a["V"], a["t1"], a["t2"], a["grad"],
+                                a["lse"], a["logp"], a["logp2"], a["ws"], a["ws_bytes"], a["err"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(h=None), INVALID), (dict(w=None), INVALID), (dict(t1=None), INVALID), (dict(logp=None), INVALID),
+    (dict(ws=None), INVALID), (dict(t2=A), INVALID), (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(V=0), INVALID),
+    (dict(H=60), UNSUPPORTED), (dict(T=1 << 24), UNSUPPORTED), (dict(V=(1 << 22) + 1), UNSUPPORTED),
+    (dict(H=(1 << 16) + 8, ldh=1 << 17, ldw=1 << 17), UNSUPPORTED),
+    (dict(ldh=56), INVALID), (dict(ldw=56), INVALID), (dict(ldh=65), INVALID), (dict(ldw=68), INVALID),
+    (dict(h=A + 8), INVALID), (dict(w=A + 2), INVALID), (dict(ws=A + 128), INVALID), (dict(t1=A + 2), INVALID),
+    (dict(logp=A + 1), INVALID), (dict(ws_bytes=1000), INVALID), (dict(T=0, h=None, ws=None), OK)])
+def test_loss_refusals(kw, status):
+    assert ce(**kw) == status
+
+
+def test_loss_workspace_one_byte_short():
+    assert ce(ws_bytes=workspace(4, 64, 100, 1) - 1) == INVALID
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(w=None), INVALID), (dict(weight=None), INVALID), (dict(dh=None), INVALID), (dict(ws=None), INVALID),
+    (dict(ldd=56), INVALID), (dict(ldd=66), INVALID), (dict(dh=A + 8), INVALID), (dict(ws_bytes=1000), INVALID),
+    (dict(H=60), UNSUPPORTED), (dict(T=0, w=None), OK)])
+def test_loss_gradient_refusals(kw, status):
+    a = dict(w=A, ldw=64, T=4, H=64, V=100, weight=A, weight2=None, dh=A, ldd=64, ws=A, ws_bytes=1 << 40)
+    a.update(kw)
+    assert L.soup_linear_ce_bwd(a["w"], a["ldw"], a["T"], a["H"], a["V"], a["weight"], a["weight2"], a["dh"], a["ldd"],
+                                a["ws"], a["ws_bytes"], None) == status
+
+
+# ------------------------------------------------------------------ AdamW
+def tensors(*rows):
+    return (_lib.AdamwTensor * max(1, len(rows)))(*[_lib.AdamwTensor(*r) for r in rows])
+
+
+def adam(rows, m=A, v=A, ms=None, vs=None, hp=None, step=1, p16=0, g16=0, count=None):
+    o = _lib.AdamwOptions(p16, g16, step, 1e-3, 0.9, 0.999, 1e-8, 0.0)
+    return L.soup_adamw_multi(tensors(*rows), len(rows) if count is None else count, ctypes.byref(o), m, v, ms, vs, hp, None)
+
+
+def test_adamw_refusals():
+    one = (A, A, None, 5)
+    assert adam([one], count=-1) == INVALID
+    assert adam([(None, A, None, 5)]) == INVALID and adam([(A, None, None, 5)]) == INVALID
+    assert adam([(A, A, None, -1)]) == INVALID
+    assert adam([(A + 2, A, None, 5)]) == INVALID and adam([(A, A + 2, None, 5)]) == INVALID
+    assert adam([(A + 1, A, None, 5)], p16=1) == INVALID and adam([(A, A, A + 1, 5)]) == INVALID
+    assert adam([one], m=None) == INVALID and adam([one], v=None) == INVALID
+    assert adam([one], m=A + 4) == INVALID and adam([one], v=A + 8) == INVALID
+    assert adam([one], ms=A) == INVALID and adam([one], vs=A) == INVALID and adam([one], ms=A + 2, vs=A) == INVALID
+    assert adam([one], step=0) == INVALID and adam([one], hp=A + 1) == INVALID
+    assert L.soup_adamw_multi(tensors(one), 1, None, A, A, None, None, None, None) == INVALID
+    assert adam([], m=None, v=None) == OK and adam([(None, None, None, 0)], m=None, v=None) == OK  # nothing to do
+
+
+def test_adamw_state_sizes():
+    n = ctypes.c_longlong()
+    assert L.soup_adamw_state_numel(tensors((A, A, None, 1), (A, A, None, 0), (A, A, None, 256), (A, A, None, 257)), 4,
+                                    ctypes.byref(n)) == OK
+    assert n.value == 256 * (1 + 0 + 1 + 2)
+    assert L.soup_adamw_state_numel(tensors((A, A, None, -2)), 1, ctypes.byref(n)) == INVALID
+    assert L.soup_adamw_state_numel(None, 1, ctypes.byref(n)) == INVALID
+    assert L.soup_adamw_state_numel(None, 0, ctypes.byref(n)) == OK and n.value == 0
+    s = M.adamw_state([1, 0, 256, 257], 8, device="cpu")
+    assert s["m"].numel() == s["v"].numel() == 1024 and s["m_scale"].numel() == 4
+    assert set(M.adamw_state([3], 32, device="cpu")) == {"m", "v"}
+    with pytest.raises(M.SoupError):
+        M.adamw_state([3], 16, device="cpu")
+
+
+def test_adamw_state_values_refusals():
+    f = L.soup_adamw_state_values
+    assert f(A, A, A, A, 100, A, A, None) == INVALID and f(A, A, A, A, -256, A, A, None) == INVALID
+    assert f(None, A, A, A, 256, A, A, None) == INVALID and f(A, A, A, A, 256, None, A, None) == INVALID
+    assert f(A + 4, A, A, A, 256, A, A, None) == INVALID and f(A, A, A, A, 256, A + 8, A, None) == INVALID
+    assert f(None, None, None, None, 0, None, None, None) == OK
+
+
+# ------------------------------------------------------------------ rotary positions
+def test_rope_frequencies():
+    d, theta, s = 128, 500000.0, 8.0
+    base = theta ** (-np.arange(0, d, 2) / d)
+    freq = lambda kind, **kw: M.rope_frequencies(M.rope_config(d, theta, scaling=kind, factor=s, **kw))
+    f, g = freq("none")
+    assert np.allclose(f, base, rtol=1e-14) and g == 1.0
+    assert np.allclose(freq("linear")[0], base / s, rtol=1e-14)
+    assert np.allclose(freq("ntk")[0], (theta * s ** (d / (d - 2))) ** (-np.arange(0, d, 2) / d), rtol=1e-13)
+    # the last pair of NTK scaling is stretched by the factor exactly
+    assert abs(freq("ntk")[0][-1] * s / base[-1] - 1) < 1e-12
+    f, g = freq("llama3", original_len=8192, low_freq_factor=1.0, high_freq_factor=4.0)
+    wave = 2 * math.pi / base
+    assert g == 1.0
+    assert np.allclose(f[wave < 8192 / 4], base[wave < 8192 / 4], rtol=1e-14)
+    assert np.allclose(f[wave > 8192], base[wave > 8192] / s, rtol=1e-14)
+    mid = (wave >= 8192 / 4) & (wave <= 8192)
+    smooth = (8192 / wave[mid] - 1) / 3
+    assert mid.sum() >= 3 and np.allclose(f[mid], (1 - smooth) * base[mid] / s + smooth * base[mid], rtol=1e-13)
+    f, g = freq("yarn", high_freq_factor=32.0)
+    assert abs(g - (0.1 * math.log(s) + 1)) < 1e-15 and f[0] == 1.0 and abs(f[-1] * s / base[-1] - 1) < 1e-12
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rotary_dim=0), INVALID), (dict(rotary_dim=-2), INVALID), (dict(theta=1.0), INVALID), (dict(theta=float("nan")), INVALID),
+    (dict(theta=float("inf")), INVALID), (dict(scaling="linear", factor=0.5), INVALID),
+    (dict(scaling="ntk", factor=float("nan")), INVALID), (dict(scaling="llama3", factor=2.0, original_len=0), INVALID),
+    (dict(scaling="yarn", factor=2.0, low_freq_factor=4.0, high_freq_factor=4.0), INVALID),
+    (dict(rotary_dim=33), UNSUPPORTED), (dict(rotary_dim=258), UNSUPPORTED), (dict(), OK)])
+def test_rope_configurations(kw, status):
+    c = M.rope_config(**{**dict(rotary_dim=64, theta=10000.0), **kw})
+    f, g = (ctypes.c_double * 256)(), ctypes.c_double()
+    assert L.soup_rope_frequencies(ctypes.byref(c), f, ctypes.byref(g)) == status
+    with pytest.raises(M.SoupError):
+        M.rope_config(64, scaling="unheard of")
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), INVALID), (dict(qo=None), INVALID), (dict(k=None), INVALID), (dict(pos=None), INVALID),
+    (dict(pos=A + 2), INVALID), (dict(T=-1), INVALID), (dict(hq=-1), INVALID), (dict(d=0), INVALID), (dict(dtype=2), INVALID),
+    (dict(dtype=-1), INVALID), (dict(d=32), UNSUPPORTED), (dict(q=A + 1), INVALID), (dict(q=A + 2, dtype=1), INVALID),
+    (dict(ldq=255), INVALID), (dict(ldko=100), INVALID), (dict(qo=A, q=A, ldqo=512), INVALID), (dict(rot=None), INVALID),
+    (dict(T=0, q=None), OK), (dict(hq=0, hk=0, q=None, k=None), OK)])
+def test_rope_refusals(kw, status):
+    a = dict(q=A, ldq=256, qo=2 * A, ldqo=256, hq=4, k=3 * A, ldk=128, ko=4 * A, ldko=128, hk=2, d=64, T=3, pos=A, dtype=0, rot=64)
+    a.update(kw)
+    c = ctypes.byref(M.rope_config(a["rot"])) if a["rot"] else None
+    assert L.soup_rope(c, a["q"], a["ldq"], a["qo"], a["ldqo"], a["hq"], a["k"], a["ldk"], a["ko"], a["ldko"], a["hk"], a["d"],
+                       a["T"], a["pos"], a["dtype"], 0, None) == status
