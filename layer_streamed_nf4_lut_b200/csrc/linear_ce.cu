@@ -32,31 +32,36 @@ namespace soup {
 namespace {
 
 constexpr int TILE = 256;            // rows and columns of a CTA pair's output tile
+constexpr int GROUP = TILE / 2;      // columns a group of four epilogue warps works through
 constexpr int BK = 64;               // k-block: 64 bf16 = one 128-byte swizzle row
 constexpr int STAGES = 6;            // operand ring
 constexpr int OPERAND = 128 * 128;   // bytes of one operand's k-block in one CTA (128 rows x 64 bf16)
 constexpr int STAGE_BYTES = 2 * OPERAND;
-constexpr int STAGING = 2 * 16384;   // epilogue: two boxes of 128 rows x 128 bytes
+constexpr int STAGING = 2 * 16384;   // epilogue: a box of 128 rows x 128 bytes for each group of four warps
 constexpr int BARRIERS = 256;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING + BARRIERS + 1024;
-constexpr int THREADS = 256;         // warp 0 TMA, 1 MMA, 2 TMEM, 3 idle, 4-7 epilogue
+constexpr int JOIN = 2 * 128 * 4;    // epilogue: the second group's sums, for the first one
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING + BARRIERS + JOIN + 1024;
+constexpr int THREADS = 384;         // warp 0 TMA, 1 MMA, 2 TMEM, 3 idle, 4-11 epilogue
+constexpr int MAX_SPLITS = 16;
+constexpr float SPLIT_COST = 0.004f;         // of a K range more
+constexpr long long ACC_BYTES = 160ll << 20; // of all accumulators, unless one for each tile takes more
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float REF_ROOM = 80.f;     // a logit may exceed its row's ref by this many powers of two:
-                                     // sums stay below 2^(80 + 17) and products with W below fp32's 2^128
+constexpr float REF_ROOM = 1.2089258e24f;  // 2^80: how far a tile's sum may lie above its ref; what is made of it
+                                           // (2^17 terms, products with W) stays below fp32's 2^128
 
 struct CeGemm {
   CUtensorMap ta, tb, to;
   const int* n_rows;  // rows in use (device)
   int n_tiles;        // output tiles of 256 columns
   int kb;             // k-blocks
-  int splits;         // gradient: K ranges, each with an accumulator of its own
-  int tcap;           // rows of one accumulator / of a part_* column
+  int kb_first;       // gradient: k-blocks of the first piece (they fix how tiles are cut)
+  int tcap;           // rows of a part_* column
   int cols;           // columns in use
   int accumulate;     // gradient: add to the accumulator instead of writing it
   int w_row0;         // first row of W of this piece
   const int2* target; // per packed row: the targets' columns (-1: none)
   const float* ref;
-  float *part_s, *part_r;  // [vocabulary tile][tcap]: the tile's sum and the ref it is against
+  float *part_s, *part_r;  // [tile of the vocabulary][tcap]: their sum and the ref it is against
   int tile0;          // first vocabulary tile of this piece
   int store_p;
   int* raised;
@@ -68,41 +73,70 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// the same, telling every epilogue thread whether all of them have `ok` (a wait that gave up in one
-// thread ends the loop for all, so that none is left alone at a barrier)
+// Barrier of the eight epilogue warps, telling each thread whether all of them have `ok`: a wait that
+// gave up in one thread ends the loop for all, so that none is left alone at a barrier.
 __device__ __forceinline__ bool epilogue_all(bool ok) {
   int all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.s32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "bar.red.and.pred q, 3, 256, p;\n\t"
       "selp.s32 %0, 1, 0, q;\n\t}"
       : "=r"(all)
       : "r"(static_cast<int>(ok))
       : "memory");
   return all != 0;
 }
+// Barrier of one group of four epilogue warps.
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+// Programmatic dependent launch: a kernel may be set up while the one before it ends; it touches
+// nothing before that one's results are there.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// One output tile of a persistent CTA pair's list.
+// K ranges of the gradient's tiles, each with an accumulator of its own: the split that leaves the
+// CTA pairs idle least, for this many tiles.
+__host__ __device__ inline int grad_splits(int m_tiles, int H, int pairs, int kb_first) {
+  const int tiles = m_tiles * ((H + TILE - 1) / TILE);
+  const long long room = ACC_BYTES / (4ll * TILE * H) / (m_tiles < 1 ? 1 : m_tiles);
+  const int most = room < MAX_SPLITS ? static_cast<int>(room) : MAX_SPLITS;
+#ifdef SPLITS
+  return SPLITS;
+#endif
+  int best = 1;
+  float cost = 1e30f;
+  for (int s = 1; s <= most && s <= kb_first; ++s) {
+    const float c = static_cast<float>((tiles * s + pairs - 1) / pairs) / s * (1.f + SPLIT_COST * s);
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
+}
+
+// One output tile, or one K range of it, of a persistent CTA pair's list: row tiles fastest and K ranges
+// slowest, so that the pairs at work read the same k-blocks at about the same time (cutting all tiles'
+// k-blocks into one equal run for each pair keeps every pair busy, but W then comes from HBM once for each
+// row tile: measured 20 % slower at 2048 rows).
 struct Unit {
-  int m, n, split, kb_lo, kb_hi;
+  int m, n, share, kb_lo, kb_hi;
 };
 template <bool GRAD>
-__device__ __forceinline__ Unit unit_of(const CeGemm& p, int m_tiles, int u) {
+__device__ __forceinline__ Unit unit_of(const CeGemm& p, int m_tiles, int splits, int u) {
   Unit t;
   t.m = u % m_tiles;
   const int r = u / m_tiles;
   t.n = r % p.n_tiles;
-  t.split = GRAD ? r / p.n_tiles : 0;
-  t.kb_lo = GRAD ? static_cast<int>(static_cast<long long>(p.kb) * t.split / p.splits) : 0;
-  t.kb_hi = GRAD ? static_cast<int>(static_cast<long long>(p.kb) * (t.split + 1) / p.splits) : p.kb;
+  t.share = r / p.n_tiles;
+  t.kb_lo = GRAD ? static_cast<int>(static_cast<long long>(p.kb) * t.share / splits) : 0;
+  t.kb_hi = GRAD ? static_cast<int>(static_cast<long long>(p.kb) * (t.share + 1) / splits) : p.kb;
   return t;
 }
 
 // 256 x 256 tiles, one CTA pair each (tcgen05 cta_group::2, M = 256, N = 256), two accumulators
 // in tensor memory so that a tile's epilogue runs beside the next tile's products.
-// GRAD = false: logits tile -> P, sums.  GRAD = true: P W -> accumulator.
+// GRAD = false: logits tile -> P, sums.  GRAD = true: P W -> accumulator of the tile's share.
 template <bool GRAD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_kernel(const __grid_constant__ CeGemm p) {
   extern __shared__ uint8_t smem_raw[];
@@ -115,10 +149,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
   uint64_t* acc_empty = bars + 2 * STAGES + 2;  // [2]; the first CTA's are used
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* join = reinterpret_cast<float*>(staging + STAGING + BARRIERS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
+  pdl_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -126,7 +162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);  // four epilogue warps in each CTA
+      mbar_init(&acc_empty[b], 16);  // eight epilogue warps in each CTA
     }
     *abort_flag = 0;
     mbar_fence_init();
@@ -140,15 +176,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();
   const int rows = *p.n_rows;
   const int m_tiles = (rows + TILE - 1) / TILE;
-  const int units = m_tiles * p.n_tiles * (GRAD ? p.splits : 1);
+  const int splits = GRAD ? grad_splits(m_tiles, p.cols, pairs, p.kb_first) : 1;
+  const int units = m_tiles * p.n_tiles * splits;
 
   if (warp == 0 && lane == 0) {
     // ---- operand loads: this CTA's 128 rows of A and its half of B's 256 columns
     int it = 0;
     for (int u = pair; u < units; u += pairs) {
-      const Unit t = unit_of<GRAD>(p, m_tiles, u);
+      const Unit t = unit_of<GRAD>(p, m_tiles, splits, u);
+      if (t.kb_lo == t.kb_hi) continue;
       const int m0 = t.m * TILE + rank * 128, n0 = t.n * TILE + rank * 128;
       for (int kb = t.kb_lo; kb < t.kb_hi; ++kb, ++it) {
         const int s = it % STAGES;
@@ -171,11 +210,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
     const uint32_t idesc = idesc_bf16(TILE, TILE, false, GRAD);
     int it = 0, n_done = 0;
     for (int u = pair; u < units; u += pairs) {
-      const Unit t = unit_of<GRAD>(p, m_tiles, u);
+      const Unit t = unit_of<GRAD>(p, m_tiles, splits, u);
       if (t.kb_lo == t.kb_hi) continue;
       const int b = n_done & 1;
+      // an accumulator's first products wait until its last ones have been read out
       if (n_done >= 2 && !mbar_wait_bounded(&acc_empty[b], ((n_done >> 1) - 1) & 1, abort_flag, p.err)) goto done;
-      tc_fence_after();
       for (int kb = t.kb_lo; kb < t.kb_hi; ++kb, ++it) {
         const int s = it % STAGES;
         if (!mbar_wait_bounded(&full[s], (it / STAGES) & 1, abort_flag, p.err)) goto done;
@@ -193,114 +232,131 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
       ++n_done;
     }
   } else if (warp >= 4) {
-    // ---- epilogue: thread = accumulator row
+    // ---- epilogue: thread = accumulator row; two groups of four warps take half of the columns each
+    const int group = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    uint8_t* my_row[2] = {staging + row * 128, staging + 16384 + row * 128};
-    const bool elected = threadIdx.x == 128;
-    int n_done = 0, boxes = 0;
+    uint8_t* box = staging + group * 16384;
+    uint8_t* my_row = box + row * 128;
+    const bool elected = (threadIdx.x & 127) == 0;
+    int n_done = 0;
     for (int u = pair; u < units; u += pairs) {
-      const Unit t = unit_of<GRAD>(p, m_tiles, u);
+      const Unit t = unit_of<GRAD>(p, m_tiles, splits, u);
       if (t.kb_lo == t.kb_hi) continue;
-      const int b = n_done & 1;
-      if (!epilogue_all(mbar_wait_bounded(&acc_full[b], (n_done >> 1) & 1, abort_flag, p.err))) goto done;
+      const int m0 = t.m * TILE + rank * 128;
+      const int buf = n_done & 1;
+      const int n0 = t.n * TILE + group * GROUP;  // this group's first column
+      if (!epilogue_all(mbar_wait_bounded(&acc_full[buf], (n_done >> 1) & 1, abort_flag, p.err))) goto done;
       tc_fence_after();
-      const uint32_t acc = tmem + lanes + b * TILE;
-      const int m0 = t.m * TILE + rank * 128, n0 = t.n * TILE;
+      const uint32_t acc = tmem + lanes + buf * TILE + group * GROUP;
       if (GRAD) {
-        for (int c = 0; c < TILE; c += 32, ++boxes) {
+        const int out_row = (t.share * m_tiles + t.m) * TILE + rank * 128;
+        for (int c = 0; c < GROUP; c += 32) {
           uint32_t v[32];
           tmem_ld32(acc + c, v);
           tmem_ld_wait();
-          if (elected) tma_store_wait_read<1>();
-          epilogue_sync();
-          uint8_t* dst = my_row[boxes & 1];
+          if (elected) tma_store_wait_read<0>();
+          group_sync(group);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(dst + ((j ^ (row & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(my_row + ((j ^ (row & 7)) << 4)) =
                 make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           fence_proxy_async_smem();
-          epilogue_sync();
+          group_sync(group);
           if (elected && n0 + c < p.cols) {
-            const uint8_t* src = staging + (boxes & 1) * 16384;
             if (p.accumulate)
-              tma_reduce_add_2d(&p.to, n0 + c, t.split * p.tcap + m0, src);
+              tma_reduce_add_2d(&p.to, n0 + c, out_row, box);
             else
-              tma_store_2d(&p.to, n0 + c, t.split * p.tcap + m0, src);
+              tma_store_2d(&p.to, n0 + c, out_row, box);
+            tma_store_commit();
           }
-          if (elected) tma_store_commit();
         }
       } else {
         const int r = m0 + row;
         const bool live = r < rows;
-        int2 tg = live ? p.target[r] : make_int2(-1, -1);  // columns of this piece (others: out of range)
-        tg.x -= p.w_row0;
-        tg.y -= p.w_row0;
-        float ref = live ? p.ref[r] : 0.f;
-        const int valid = p.cols - n0;  // columns of this tile inside the vocabulary
-        // the largest logit that takes part: only to see whether ref has room for it
-        float mx = -INFINITY;
-        for (int c = 0; c < TILE; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(acc + c, v);
-          tmem_ld_wait();
+        const int2 tg = live ? p.target[r] : make_int2(-1, -1);
+        const int ta = tg.x - p.w_row0 - n0, tb = tg.y - p.w_row0 - n0;  // the targets' columns here
+        const int valid = p.cols - n0;                                    // columns inside the vocabulary
+        float ref = live ? p.ref[r] : 0.f, total = 0.f;
+        for (int attempt = 0; attempt < 2; ++attempt) {
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int c = 0; c < GROUP; c += 64) {
+            uint32_t w[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int col = c + j;
-            const float x = (col < valid && n0 + col != tg.x && n0 + col != tg.y) ? __uint_as_float(v[j]) : -INFINITY;
-            mx = fmaxf(mx, x);
+            for (int half = 0; half < 2; ++half) {
+              uint32_t v[32];
+              const int c1 = c + 32 * half;
+              tmem_ld32(acc + c1, v);
+              tmem_ld_wait();
+              // columns that stay out: the targets', for the few rows that have one here, and those past the end
+              const int a = ta - c1, b = tb - c1;
+              if (__any_sync(0xffffffffu, (a >= 0 && a < 32) || (b >= 0 && b < 32)) || c1 + 32 > valid) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (j == a || j == b || c1 + j >= valid) v[j] = 0xff800000u;  // -inf
+              }
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float e0 = exp2_approx(fmaf(__uint_as_float(v[j]), LOG2E, -ref));
+                const float e1 = exp2_approx(fmaf(__uint_as_float(v[j + 1]), LOG2E, -ref));
+                sum[j & 3] += e0;
+                sum[(j + 1) & 3] += e1;
+                w[16 * half + (j >> 1)] = pack_bf16x2(e0, e1);
+              }
+            }
+            if (p.store_p) {
+              if (elected) tma_store_wait_read<0>();
+              group_sync(group);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(my_row + ((j ^ (row & 7)) << 4)) =
+                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+              fence_proxy_async_smem();
+              group_sync(group);
+              if (elected) {
+                tma_store_2d(&p.to, n0 + c, m0, box);
+                tma_store_commit();
+              }
+            }
           }
-        }
-        mx *= LOG2E;
-        if (live && mx - ref > REF_ROOM) {
-          ref = ceilf(mx);
-          *p.raised = 1;
-        }
-        __syncwarp();
-        float sum = 0.f;
-        for (int c = 0; c < TILE; c += 64, ++boxes) {
-          uint32_t w[32];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          // A logit far above ref (an infinite sum counts): once more, against the row's largest logit here
+          const bool over = live && total > REF_ROOM;
+          float* theirs = join + 128 * buf + row;  // one for each accumulator
+          if (group == 1) *theirs = total;
+          if (epilogue_all(!over) || attempt == 1) {
+            if (group == 0) total += *theirs;
+            break;
+          }
+          float top = -INFINITY;
+          for (int c = 0; c < GROUP; c += 32) {
             uint32_t v[32];
-            tmem_ld32(acc + c + 32 * half, v);
+            tmem_ld32(acc + c, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              float e[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int col = c + 32 * half + j + k;
-                e[k] = exp2_approx(fmaf(__uint_as_float(v[j + k]), LOG2E, -ref));
-                if (col >= valid || n0 + col == tg.x || n0 + col == tg.y) e[k] = 0.f;
-                sum += e[k];
-              }
-              w[16 * half + (j >> 1)] = pack_bf16x2(e[0], e[1]);
-            }
+            for (int j = 0; j < 32; ++j)
+              if (c + j != ta && c + j != tb && c + j < valid) top = fmaxf(top, __uint_as_float(v[j]));
           }
-          if (p.store_p) {
-            if (elected) tma_store_wait_read<1>();
-            epilogue_sync();
-            uint8_t* dst = my_row[boxes & 1];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(dst + ((j ^ (row & 7)) << 4)) =
-                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            fence_proxy_async_smem();
-            epilogue_sync();
-            if (elected) {
-              tma_store_2d(&p.to, n0 + c, m0, staging + (boxes & 1) * 16384);
-              tma_store_commit();
-            }
+          if (elected) tma_store_wait_all();  // the boxes are written again, here and below: in order
+          group_sync(group);
+          *reinterpret_cast<float2*>(my_row) = make_float2(top, over ? 1.f : 0.f);
+          epilogue_all(true);
+          const float2 other = *reinterpret_cast<const float2*>(staging + (1 - group) * 16384 + row * 128);
+          epilogue_all(true);
+          if (over || other.y != 0.f) {
+            ref = ceilf(fmaxf(top, other.x) * LOG2E);
+            *p.raised = 1;
           }
         }
-        const long long at = static_cast<long long>(p.tile0 + t.n) * p.tcap + r;
-        p.part_s[at] = sum;
-        p.part_r[at] = ref;
+        if (group == 0) {
+          const long long at = static_cast<long long>(p.tile0 + t.n) * p.tcap + r;
+          p.part_s[at] = total;
+          p.part_r[at] = ref;
+        }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[b], 0));
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
       ++n_done;
     }
     if (elected) tma_store_wait_all();
@@ -351,6 +407,8 @@ __global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh,
   __shared__ float red[32];
   __shared__ int before;
   const int t = blockIdx.x;
+  pdl_launch();
+  pdl_wait();
   if (threadIdx.x == 0) before = 0;
   __syncthreads();
   int n = 0;
@@ -404,20 +462,24 @@ __global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh,
 }
 
 // Rows that met a logit beyond their ref's room: P of this piece and the accumulators go to the
-// largest ref a tile took.  Powers of two: exact.  One warp per row; nothing to do while the
+// largest ref a part took.  Powers of two: exact.  One warp per row; nothing to do while the
 // piece's flag is down.
-__global__ void ce_raise_kernel(const int* __restrict__ raised, const int* __restrict__ n_rows, int tile0, int tiles,
+__global__ void ce_raise_kernel(const int* __restrict__ raised, const int* __restrict__ n_rows, int tile0, int parts,
                                 int tcap, const float* __restrict__ part_r, float* __restrict__ ref,
-                                uint16_t* __restrict__ P, long long ldp, float* __restrict__ acc, int splits, int H,
+                                uint16_t* __restrict__ P, long long ldp, float* __restrict__ acc, int pairs, int kb_first, int H,
                                 int accumulated) {
+  pdl_launch();
+  pdl_wait();
   if (*raised == 0) return;
+  const int rows = *n_rows, m_tiles = (rows + TILE - 1) / TILE;
+  const int splits = grad_splits(m_tiles, H, pairs, kb_first);
   const int lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x >> 5);
-  for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < *n_rows; r += warps) {
+  for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows; r += warps) {
     float top = ref[r];
-    for (int i = lane; i < tiles; i += 32) top = fmaxf(top, part_r[static_cast<long long>(tile0 + i) * tcap + r]);
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, part_r[static_cast<long long>(tile0 + i) * tcap + r]);
     top = warp_max(top);
     if (!(top > ref[r])) continue;
-    for (int i = 0; i < tiles; ++i) {
+    for (int i = 0; i < parts; ++i) {
       const float have = part_r[static_cast<long long>(tile0 + i) * tcap + r];
       if (have == top) continue;
       const float f = exp2f(have - top);
@@ -429,45 +491,59 @@ __global__ void ce_raise_kernel(const int* __restrict__ raised, const int* __res
     }
     if (accumulated) {
       const float f = exp2f(ref[r] - top);
-      for (int s = 0; s < splits; ++s) {
-        float* a = acc + (static_cast<long long>(s) * tcap + r) * H;
-        for (int c = lane; c < H; c += 32) a[c] *= f;
-      }
+      const int m = r / TILE;
+      for (int c = lane; c < H; c += 32)
+        for (int j = 0; j < splits; ++j) acc[(static_cast<long long>(j * m_tiles + m) * TILE + r % TILE) * H + c] *= f;
     }
     __syncwarp();
     if (lane == 0) ref[r] = top;
   }
 }
 
-// Sums of each row's tiles (32 rows per block: lane = row, the warps share the tiles and their sums
+// Sums of each row's parts (32 rows per block: lane = row, the warps share the parts and their sums
 // are added in warp order), log-probs and lse.  The scalars of a row are formed in 64 bits.
-__global__ void ce_stats_kernel(const int* __restrict__ n_rows, int tiles, int tcap, const float* __restrict__ part_s,
+constexpr int STATS_WARPS = 32;
+__global__ void __launch_bounds__(32 * STATS_WARPS) ce_stats_kernel(const int* __restrict__ n_rows, int parts, int tcap, const float* __restrict__ part_s,
                                 const float* __restrict__ part_r, CeRows rows, float* __restrict__ out_lse,
                                 float* __restrict__ out_logp, float* __restrict__ out_logp2) {
-  __shared__ float sums[8][32], refs[8][32];
+  __shared__ float sums[STATS_WARPS][32], refs[STATS_WARPS][32];
+  pdl_launch();
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = blockIdx.x * 32 + lane;
   const bool live = r < *n_rows;
   float top = -INFINITY, sum = 0.f;
   if (live) {
     top = rows.ref[r];
-    for (int i = warp; i < tiles; i += 8) {
-      const long long at = static_cast<long long>(i) * tcap + r;
-      const float s = part_s[at], k = part_r[at];
-      if (k > top) {
-        sum *= exp2f(top - k);
-        top = k;
+    // eight parts at a time, so that their loads are in flight together
+    for (int i = warp; i < parts; i += 8 * STATS_WARPS) {
+      float s[8], k[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int q = i + j * STATS_WARPS;
+        const long long at = static_cast<long long>(q) * tcap + r;
+        s[j] = q < parts ? part_s[at] : 0.f;
+        k[j] = q < parts ? part_r[at] : top;
       }
-      sum += s * exp2f(k - top);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (k[j] > top) {
+          sum *= exp2f(top - k[j]);
+          top = k[j];
+        }
+        sum += k[j] == top ? s[j] : s[j] * exp2f(k[j] - top);
+      }
     }
   }
   sums[warp][lane] = sum;
   refs[warp][lane] = top;
   __syncthreads();
   if (warp != 0 || !live) return;
-  for (int i = 1; i < 8; ++i) top = fmaxf(top, refs[i][lane]);
+  for (int i = 1; i < STATS_WARPS; ++i) top = fmaxf(top, refs[i][lane]);
   double other = 0.0;
-  for (int i = 0; i < 8; ++i) other += static_cast<double>(sums[i][lane]) * exp2(static_cast<double>(refs[i][lane] - top));
+  for (int i = 0; i < STATS_WARPS; ++i)
+    other += static_cast<double>(sums[i][lane]) *
+             (refs[i][lane] == top ? 1.0 : exp2(static_cast<double>(refs[i][lane] - top)));
   const int2 tg = rows.target[r];
   const bool two = tg.y >= 0 && tg.y != tg.x;
   const double ln2 = 0.6931471805599453;
@@ -486,12 +562,15 @@ __global__ void ce_stats_kernel(const int* __restrict__ n_rows, int tiles, int t
   if (out_logp2) out_logp2[t] = tg.y >= 0 ? static_cast<float>(lpb) : 0.f;
 }
 
-// dh of one row of the batch per block: the accumulators of the K ranges, added in order, and the
+// dh of one row of the batch per block: the accumulators of the tile's shares, added in order, and the
 // targets' rows of W with coefficients formed from 1 - p.
 __global__ void ce_dh_kernel(const int* __restrict__ place, CeRows rows, const float* __restrict__ weight,
-                             const float* __restrict__ weight2, const float* __restrict__ acc, int splits, int tcap,
+                             const float* __restrict__ weight2, const float* __restrict__ acc,
+                             const int* __restrict__ n_rows, int pairs, int kb_first,
                              const uint16_t* __restrict__ w, long long ldw, int H, uint16_t* __restrict__ dh,
                              long long ldd) {
+  pdl_launch();
+  pdl_wait();
   const int t = blockIdx.x;
   uint16_t* out = dh + t * ldd;
   const int r = place[t];
@@ -513,12 +592,15 @@ __global__ void ce_dh_kernel(const int* __restrict__ place, CeRows rows, const f
   const float cb = two ? w1 * pb.x - w2 * pb.y : 0.f;
   const uint16_t* wa = w + tg.x * ldw;
   const uint16_t* wb = w + (two ? tg.y : tg.x) * ldw;
+  const int m_tiles = (*n_rows + TILE - 1) / TILE, m = r / TILE;
+  const int splits = grad_splits(m_tiles, H, pairs, kb_first);
   for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
     for (int s = 0; s < splits; ++s) {
-      const float4* q = reinterpret_cast<const float4*>(acc + (static_cast<long long>(s) * tcap + r) * H + c);
+      const float4* q = reinterpret_cast<const float4*>(
+          acc + (static_cast<long long>(s * m_tiles + m) * TILE + r % TILE) * H + c);
       const float4 x = q[0], y = q[1];
       v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
       v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
@@ -538,14 +620,14 @@ __global__ void ce_dh_kernel(const int* __restrict__ place, CeRows rows, const f
 }
 
 // ---------------------------------------------------------------- the plan
-constexpr int ROW_BLOCK = 4096;                       // rows that share one walk over the vocabulary
-constexpr long long P_BYTES = 64ll << 20;             // of one piece's P: half of the L2
-constexpr int MAX_SPLITS = 4;
+constexpr int ROW_BLOCK = 4096;           // rows that share one walk over the vocabulary
+constexpr long long P_BYTES = 64ll << 20; // of one piece's P: half of the L2
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct CePlan {
-  int block, blocks, tcap, tiles, piece_tiles, pieces, splits;
+  int pairs, block, blocks, tcap, tiles, piece_tiles, pieces, h_tiles, kb_first;
+  long long acc_rows;
   // byte offsets: per row block (stride per_block), then shared by the blocks
   size_t n_rows, place, target, row, ref, la, lb, inv_z, pa, pb, acc, per_block;
   size_t raised, packed, part_s, part_r, p, total;
@@ -553,34 +635,24 @@ struct CePlan {
 
 CePlan ce_plan(int T, int H, int V, bool grad, int sms) {
   CePlan q{};
-  const int pairs = sms > 1 ? sms / 2 : 74;
+  q.pairs = sms > 1 ? sms / 2 : 74;
   q.block = std::min(std::max(T, 1), ROW_BLOCK);
   q.blocks = (std::max(T, 1) + q.block - 1) / q.block;
   q.tcap = (q.block + TILE - 1) / TILE * TILE;
   q.tiles = (V + TILE - 1) / TILE;
+  q.h_tiles = (H + TILE - 1) / TILE;
   const int mt = q.tcap / TILE;
+  q.piece_tiles = q.tiles;
   if (grad) {
     // a piece's tiles fill whole waves of CTA pairs, as many as P's bytes allow
     const long long most = std::max(1ll, P_BYTES / (static_cast<long long>(q.tcap) * TILE * 2));
     long long n = std::min<long long>(most, q.tiles);
-    const long long waves = n * mt / pairs;
-    if (waves >= 1 && n < q.tiles) n = waves * pairs / mt;
+    const long long waves = n * mt / q.pairs;
+    if (waves >= 1 && n < q.tiles) n = waves * q.pairs / mt;
     q.piece_tiles = static_cast<int>(std::max(1ll, n));
-    // K ranges of the gradient's tiles: the fewest that fill the last wave of pairs
-    const int units = mt * ((H + TILE - 1) / TILE);
-    double best = 1e30;
-    q.splits = 1;
-    const int kb = (std::min(V, q.piece_tiles * TILE) + BK - 1) / BK;  // of the first piece: no range is empty in it
-    for (int s = 1; s <= std::min(MAX_SPLITS, kb); ++s) {
-      const double cost = static_cast<double>((units * s + pairs - 1) / pairs) / s * (1.0 + 0.02 * s);
-      if (cost < best) {
-        best = cost;
-        q.splits = s;
-      }
-    }
-  } else {
-    q.piece_tiles = q.tiles;
-    q.splits = 0;
+    q.kb_first = (std::min(V, q.piece_tiles * TILE) + BK - 1) / BK;
+    for (int m = 1; m <= mt; ++m)  // whatever the number of rows with targets turns out to be
+      q.acc_rows = std::max(q.acc_rows, static_cast<long long>(TILE) * m * grad_splits(m, H, q.pairs, q.kb_first));
   }
   q.pieces = (q.tiles + q.piece_tiles - 1) / q.piece_tiles;
   size_t o = 0;
@@ -600,7 +672,7 @@ CePlan ce_plan(int T, int H, int V, bool grad, int sms) {
   q.inv_z = take(rows * 4);
   q.pa = take(rows * 8);
   q.pb = take(rows * 8);
-  q.acc = take(static_cast<size_t>(q.splits) * rows * H * 4);
+  q.acc = take(static_cast<size_t>(q.acc_rows) * H * 4);
   q.per_block = o;
   o *= q.blocks;
   q.raised = take(static_cast<size_t>(q.pieces) * 4);
@@ -627,6 +699,24 @@ int row_threads(int h) { return std::max(32, std::min(512, (h / 8 + 31) / 32 * 3
     if (e_ != cudaSuccess) return e_;     \
   } while (0)
 
+// A launch that may be set up while the one before it on the stream ends (every kernel here waits for
+// that one's results before it touches memory).
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), int grid, int threads, int smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(static_cast<unsigned>(grid));
+  c.blockDim = dim3(static_cast<unsigned>(threads));
+  c.dynamicSmemBytes = static_cast<size_t>(smem);
+  c.stream = st;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a;
+  c.numAttrs = 1;
+  ++g_kernel_launches;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<Params>(args)...);
+}
+
 cudaError_t gemm_attributes() {
   // per device and cheap, so set before each call: two function attributes
   CE_CK(cudaFuncSetAttribute(ce_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
@@ -640,8 +730,7 @@ size_t linear_ce_workspace(int T, int H, int V, bool grad) { return ce_plan(T, H
 cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_t* w, long long ldw, int T, int H, int V,
                                  const int32_t* t1, const int32_t* t2, bool grad, float* lse, float* logp, float* logp2,
                                  uint8_t* ws, int* err, cudaStream_t st) {
-  const int sms = device_sm_count();
-  const CePlan q = ce_plan(T, H, V, grad, sms);
+  const CePlan q = ce_plan(T, H, V, grad, device_sm_count());
   CE_CK(gemm_attributes());
   int* raised = reinterpret_cast<int*>(ws + q.raised);
   uint16_t* packed = reinterpret_cast<uint16_t*>(ws + q.packed);
@@ -657,55 +746,45 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
     return cudaErrorInvalidValue;
   b.ta = a.to;
   a.kb = (H + BK - 1) / BK;
-  a.tcap = b.tcap = q.tcap;
+  a.tcap = q.tcap;
   a.part_s = part_s;
   a.part_r = part_r;
   a.store_p = grad;
   a.err = b.err = err;
-  b.n_tiles = (H + TILE - 1) / TILE;
-  b.splits = q.splits;
+  b.n_tiles = q.h_tiles;
+  b.kb_first = q.kb_first;
   b.cols = H;
-  const dim3 grid(2 * std::max(1, sms / 2));
   for (int k = 0; k < q.blocks; ++k) {
-    const int t0 = k * q.block, n = std::min(q.block, T - t0);
+    const int t0 = k * q.block, n = std::min(q.block, T - t0), mt = (n + TILE - 1) / TILE;
     uint8_t* base = ws + k * q.per_block;
     const CeRows rows = rows_of(q, base);
     int* n_rows = reinterpret_cast<int*>(base + q.n_rows);
     float* acc = reinterpret_cast<float*>(base + q.acc);
-    ce_prepare_kernel<<<n, row_threads(H), 0, st>>>(h + t0 * ldh, ldh, w, ldw, n, H, V, t1 + t0, t2 ? t2 + t0 : nullptr,
-                                                    packed, rows, reinterpret_cast<int*>(base + q.place), n_rows, raised,
-                                                    q.pieces, lse ? lse + t0 : nullptr, logp + t0,
-                                                    logp2 ? logp2 + t0 : nullptr, err);
-    CE_CK(cudaGetLastError());
-    ++g_kernel_launches;
-    if (grad && !tma_encode_sw128(&b.to, acc, true, H, static_cast<unsigned long long>(q.splits) * q.tcap, 4ull * H, 32, 128))
+    CE_CK(launch(ce_prepare_kernel, n, row_threads(H), 0, st, h + t0 * ldh, ldh, w, ldw, n, H, V, t1 + t0,
+                 t2 ? t2 + t0 : nullptr, packed, rows, reinterpret_cast<int*>(base + q.place), n_rows, raised, q.pieces,
+                 lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr, err));
+    if (grad && !tma_encode_sw128(&b.to, acc, true, H, static_cast<unsigned long long>(q.acc_rows), 4ull * H, 32, 128))
       return cudaErrorInvalidValue;
     a.n_rows = b.n_rows = n_rows;
     a.target = rows.target;
     a.ref = rows.ref;
     for (int i = 0; i < q.pieces; ++i) {
-      a.tile0 = i * q.piece_tiles;
-      a.n_tiles = std::min(q.piece_tiles, q.tiles - a.tile0);
-      a.w_row0 = b.w_row0 = a.tile0 * TILE;
+      const int tile0 = i * q.piece_tiles;
+      a.n_tiles = std::min(q.piece_tiles, q.tiles - tile0);
+      a.tile0 = tile0;
+      a.w_row0 = b.w_row0 = tile0 * TILE;
       a.cols = std::min(V - a.w_row0, a.n_tiles * TILE);
       a.raised = raised + i;
-      ce_gemm_kernel<false><<<grid, THREADS, SMEM_BYTES, st>>>(a);
-      CE_CK(cudaGetLastError());
-      ++g_kernel_launches;
+      CE_CK(launch(ce_gemm_kernel<false>, 2 * std::min(q.pairs, mt * a.n_tiles), THREADS, SMEM_BYTES, st, a));
       if (!grad) continue;
-      ce_raise_kernel<<<64, 256, 0, st>>>(raised + i, n_rows, a.tile0, a.n_tiles, q.tcap, part_r, rows.ref, P, ldp, acc,
-                                          q.splits, H, i > 0);
-      CE_CK(cudaGetLastError());
+      CE_CK(launch(ce_raise_kernel, 64, 256, 0, st, raised + i, n_rows, a.tile0, a.n_tiles, q.tcap, part_r,
+                   rows.ref, P, ldp, acc, q.pairs, q.kb_first, H, i > 0));
       b.kb = (a.cols + BK - 1) / BK;
       b.accumulate = i > 0;
-      ce_gemm_kernel<true><<<grid, THREADS, SMEM_BYTES, st>>>(b);
-      CE_CK(cudaGetLastError());
-      g_kernel_launches += 2;
+      CE_CK(launch(ce_gemm_kernel<true>, 2 * q.pairs, THREADS, SMEM_BYTES, st, b));
     }
-    ce_stats_kernel<<<(n + 31) / 32, 256, 0, st>>>(n_rows, q.tiles, q.tcap, part_s, part_r, rows, lse ? lse + t0 : nullptr,
-                                                   logp + t0, logp2 ? logp2 + t0 : nullptr);
-    CE_CK(cudaGetLastError());
-    ++g_kernel_launches;
+    CE_CK(launch(ce_stats_kernel, (n + 31) / 32, 32 * STATS_WARPS, 0, st, n_rows, q.tiles, q.tcap, part_s, part_r, rows,
+                 lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr));
   }
   return cudaSuccess;
 }
@@ -716,11 +795,9 @@ cudaError_t linear_ce_bwd_launch(const uint16_t* w, long long ldw, int T, int H,
   for (int k = 0; k < q.blocks; ++k) {
     const int t0 = k * q.block, n = std::min(q.block, T - t0);
     uint8_t* base = ws + k * q.per_block;
-    ce_dh_kernel<<<n, row_threads(H), 0, st>>>(reinterpret_cast<int*>(base + q.place), rows_of(q, base), weight + t0,
-                                               weight2 ? weight2 + t0 : nullptr, reinterpret_cast<float*>(base + q.acc),
-                                               q.splits, q.tcap, w, ldw, H, dh + t0 * ldd, ldd);
-    CE_CK(cudaGetLastError());
-    ++g_kernel_launches;
+    CE_CK(launch(ce_dh_kernel, n, row_threads(H), 0, st, reinterpret_cast<int*>(base + q.place), rows_of(q, base),
+                 weight + t0, weight2 ? weight2 + t0 : nullptr, reinterpret_cast<float*>(base + q.acc),
+                 reinterpret_cast<int*>(base + q.n_rows), q.pairs, q.kb_first, w, ldw, H, dh + t0 * ldd, ldd));
   }
   return cudaSuccess;
 }
