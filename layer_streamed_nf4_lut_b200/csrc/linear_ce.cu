@@ -43,8 +43,7 @@ constexpr int JOIN = 2 * 128 * 4;    // epilogue: the second group's sums, for t
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING + BARRIERS + JOIN + 1024;
 constexpr int THREADS = 384;         // warp 0 TMA, 1 MMA, 2 TMEM, 3 idle, 4-11 epilogue
 constexpr int MAX_SPLITS = 16;
-constexpr float SPLIT_COST = 0.004f;         // of a K range more
-constexpr long long ACC_BYTES = 160ll << 20; // of all accumulators, unless one for each tile takes more
+constexpr long long ACC_BYTES = 144ll << 20; // of all accumulators, unless one for each tile takes more
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float REF_ROOM = 1.2089258e24f;  // 2^80: how far a tile's sum may lie above its ref; what is made of it
                                            // (2^17 terms, products with W) stays below fp32's 2^128
@@ -94,19 +93,20 @@ __device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// K ranges of the gradient's tiles, each with an accumulator of its own: the split that leaves the
-// CTA pairs idle least, for this many tiles.
+// K ranges of the gradient's tiles, each with an accumulator of its own.  A range costs its k-blocks and
+// about 10 more for its epilogue; pairs that idle cost time only below 93 % of them at work, because
+// the clock rises under the power limit when fewer work.  Measured, 1 / 2 / 3 ranges: 1108 / 901 / 977 us
+// at 512 x 4096 x 128256 (32 tiles on 74 pairs), 1691 / 1720 / 1734 at 1024, 2700 / 2530 / 2490 at 1500,
+// 6566 / 6430 / 6683 at 2048 x 8192, 1793 / 1842 / 1908 at 4096 x 2048 x 64000.
 __host__ __device__ inline int grad_splits(int m_tiles, int H, int pairs, int kb_first) {
   const int tiles = m_tiles * ((H + TILE - 1) / TILE);
   const long long room = ACC_BYTES / (4ll * TILE * H) / (m_tiles < 1 ? 1 : m_tiles);
   const int most = room < MAX_SPLITS ? static_cast<int>(room) : MAX_SPLITS;
-#ifdef SPLITS
-  return SPLITS;
-#endif
   int best = 1;
   float cost = 1e30f;
   for (int s = 1; s <= most && s <= kb_first; ++s) {
-    const float c = static_cast<float>((tiles * s + pairs - 1) / pairs) / s * (1.f + SPLIT_COST * s);
+    const float busy = static_cast<float>(tiles * s), wide = 0.93f * ((tiles * s + pairs - 1) / pairs * pairs);
+    const float c = (busy > wide ? busy : wide) * (static_cast<float>(kb_first) / s + 10.f);
     if (c < cost) {
       cost = c;
       best = s;
@@ -621,7 +621,7 @@ __global__ void ce_dh_kernel(const int* __restrict__ place, CeRows rows, const f
 
 // ---------------------------------------------------------------- the plan
 constexpr int ROW_BLOCK = 4096;           // rows that share one walk over the vocabulary
-constexpr long long P_BYTES = 64ll << 20; // of one piece's P: half of the L2
+constexpr long long P_BYTES = 96ll << 20; // of one piece's P: half of the L2
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
