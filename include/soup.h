@@ -366,7 +366,7 @@ soup_status soup_linear_ce_bwd(const void* w, long long ldw, int T, int hidden, 
  * lr, 1/(1-b1^step), 1/(1-b2^step) read on the device in place of lr and step, for captured graphs.
  * tensors is a host array, read during the call.  A tensor of n = 0 is allowed.  SOUP_ERR_INVALID_ARG
  * for null pointers, n < 0, step < 1 (without hp), v_scale without m_scale or the reverse, a
- * state address not 16-byte aligned, or tensors not aligned to their own type. */
+ * state address not 32-byte aligned, or tensors not aligned to their own type. */
 #define SOUP_ADAMW_BLOCK 256
 typedef struct soup_adamw_tensor {
   void* p;               /* device, n elements, updated in place */

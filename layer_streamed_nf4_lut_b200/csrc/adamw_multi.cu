@@ -24,6 +24,7 @@ namespace soup {
 namespace {
 
 constexpr int BLOCK = ADAMW_BLOCK;
+constexpr int WARPS = 8;              // of a thread block; a warp works one block of elements at a time
 constexpr int LAUNCH_TENSORS = 640;  // descriptors of one launch: 32 KB of kernel parameters hold 800
 
 struct AdamTensor {
@@ -31,7 +32,7 @@ struct AdamTensor {
   const void* g;
   uint16_t* pb;
   long long n;
-  int aligned;  // p, g and pb on 16 bytes
+  int aligned;  // p, g and pb for 8 elements in one access
 };
 struct Hyper {
   float lr, b1, b2, g1, g2, eps, wd, bc1, bc2;  // g = 1 - b
@@ -55,10 +56,11 @@ __device__ __forceinline__ void store_f(uint16_t* p, float v) {
   const __nv_bfloat16 b = __float2bfloat16_rn(v);
   *p = *reinterpret_cast<const uint16_t*>(&b);
 }
+// 32 bytes a lane in one instruction (p on 32 bytes)
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p));
 }
 __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
   const uint4 u = *reinterpret_cast<const uint4*>(p);
@@ -71,8 +73,9 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
   }
 }
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) =
@@ -87,12 +90,24 @@ __device__ __forceinline__ float v_value(int q, float scale) {
   const float r = static_cast<float>(q) * (1.f / 255.f), r2 = r * r;
   return r2 * r2 * scale;
 }
-// x / scale for 0 <= x <= scale, also where 1 / scale leaves fp32's range
+// Square root and quotient to about 2^-22: the step they make is lr times a number near 1, and a code
+// is 8 bits, while the correctly rounded forms make the 8-bit kernel bound by its arithmetic.
+__device__ __forceinline__ float root(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float root_ftz(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// to x / scale for 0 <= x <= scale, also where 1 / scale leaves fp32's range
 struct Ratio {
   float up, inv;
-  __device__ explicit Ratio(float scale) {
-    up = scale < 1e-30f ? 18446744073709551616.f : 1.f;
-    inv = scale > 0.f ? 1.f / (scale * up) : 0.f;
+  __device__ Ratio(float scale, float to) {
+    up = scale < 1e-25f ? 18446744073709551616.f : 1.f;
+    inv = scale > 0.f ? to / (scale * up) : 0.f;
   }
   __device__ float operator()(float x) const { return x * up * inv; }
 };
@@ -105,80 +120,118 @@ __device__ __forceinline__ float block_top(const float (&x)[8]) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
 }
 
+// A block whose tensor is not aligned for wide accesses, or ends in it: lanes take neighbouring elements
+// (j * 32 + lane), and shared memory turns them into 8 a lane and back.
+template <typename E>
+__device__ __forceinline__ void load_strided(const E* p, int n, int lane, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j * 32 + lane < n ? load_f(p + j * 32 + lane) : 0.f;
+}
+template <typename E>
+__device__ __forceinline__ void store_strided(E* p, int n, int lane, const float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j * 32 + lane < n) store_f(p + j * 32 + lane, v[j]);
+}
+__device__ __forceinline__ void to_own(float* sm, int lane, float (&v)[8]) {
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sm[j * 32 + lane] = v[j];
+  __syncwarp();
+  const float4 a = reinterpret_cast<const float4*>(sm)[2 * lane], b = reinterpret_cast<const float4*>(sm)[2 * lane + 1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void to_strided(float* sm, int lane, float (&v)[8]) {
+  __syncwarp();
+  reinterpret_cast<float4*>(sm)[2 * lane] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(sm)[2 * lane + 1] = make_float4(v[4], v[5], v[6], v[7]);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = sm[j * 32 + lane];
+}
+
 template <typename P, typename G, bool BITS8>
-__global__ void __launch_bounds__(256) adamw_multi_kernel(const __grid_constant__ AdamArgs a) {
+__global__ void __launch_bounds__(32 * WARPS) adamw_multi_kernel(const __grid_constant__ AdamArgs a) {
+  __shared__ __align__(16) float turn[WARPS][BLOCK];
   const int lane = threadIdx.x & 31;
-  const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
-  const long long w = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  // a run of blocks per warp
-  const long long lo = a.blocks * w / warps, hi = a.blocks * (w + 1) / warps;
-  if (lo >= hi) return;
+  float* sm = turn[threadIdx.x >> 5];
+  const long long stride = static_cast<long long>(gridDim.x) * WARPS;
   Hyper k = a.k;
   if (a.hp) {
     k.lr = a.hp[0];
     k.bc1 = a.hp[1];
     k.bc2 = a.hp[2];
   }
-  int i = 0;  // the tensor of block lo
-  for (int step = 512; step > 0; step >>= 1)
-    if (i + step < a.count && a.first[i + step] <= lo) i += step;
-  for (long long b = lo; b < hi; ++b) {
-    while (i + 1 < a.count && a.first[i + 1] <= b) ++i;
+  int i = 0;  // the tensor of block b
+  // blocks that are worked at one time lie side by side, which keeps DRAM pages open
+  for (long long b = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); b < a.blocks; b += stride) {
+    if (i + 1 < a.count && a.first[i + 1] <= b)
+#pragma unroll 1
+      for (int step = 512; step > 0; step >>= 1)
+        if (i + step < a.count && a.first[i + step] <= b) i += step;
     const AdamTensor& t = a.t[i];
-    const long long e = (b - a.first[i]) * BLOCK + lane * 8;  // this lane's first element
-    const int n = static_cast<int>(max(0ll, min(8ll, t.n - e)));
-    const long long at = (a.block0 + b) * BLOCK + lane * 8;   // ... and its place in the states
-    P* p = static_cast<P*>(t.p) + e;
-    const G* g = static_cast<const G*>(t.g) + e;
+    const long long e0 = (b - a.first[i]) * BLOCK, e = e0 + lane * 8;
+    const int nb = static_cast<int>(min(static_cast<long long>(BLOCK), t.n - e0));  // elements of this block, > 0
+    const int n = max(0, min(8, nb - lane * 8));
+    const long long at = (a.block0 + b) * BLOCK + lane * 8;  // this lane's place in the states
+    P* p = static_cast<P*>(t.p);
+    const G* g = static_cast<const G*>(t.g);
     float pv[8], gv[8], m[8], v[8];
-    const bool whole = n == 8 && t.aligned;
-    if (whole) {
-      load8(p, pv);
-      load8(g, gv);
+    const bool whole = nb == BLOCK && t.aligned;
+    uint2 mq, vq;
+    float ms, vs;
+    if (BITS8) {
+      mq = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.m) + at);
+      vq = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.v) + at);
+      ms = a.m_scale[a.block0 + b];
+      vs = a.v_scale[a.block0 + b];
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        pv[j] = j < n ? load_f(p + j) : 0.f;
-        gv[j] = j < n ? load_f(g + j) : 0.f;
-      }
+      load8(static_cast<const float*>(a.m) + at, m);
+      load8(static_cast<const float*>(a.v) + at, v);
+    }
+    if (whole) {
+      load8(p + e, pv);
+      load8(g + e, gv);
+    } else {
+      load_strided(p + e0, nb, lane, pv);
+      load_strided(g + e0, nb, lane, gv);
+      to_own(sm, lane, pv);
+      to_own(sm, lane, gv);
     }
     if (BITS8) {
-      const uint2 mq = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.m) + at);
-      const uint2 vq = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.v) + at);
-      const float ms = a.m_scale[a.block0 + b], vs = a.v_scale[a.block0 + b];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t mw = (j < 4 ? mq.x : mq.y) >> (8 * (j & 3)), vw = (j < 4 ? vq.x : vq.y) >> (8 * (j & 3));
         m[j] = m_value(static_cast<int8_t>(mw & 255u), ms);
         v[j] = v_value(static_cast<int>(vw & 255u), vs);
       }
-    } else {
-      load8(static_cast<const float*>(a.m) + at, m);
-      load8(static_cast<const float*>(a.v) + at, v);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       m[j] = k.b1 * m[j] + k.g1 * gv[j];
       v[j] = k.b2 * v[j] + k.g2 * gv[j] * gv[j];
       const float mh = m[j] * k.bc1, vh = v[j] * k.bc2;
-      pv[j] = pv[j] - k.lr * (mh / (sqrtf(vh) + k.eps) + k.wd * pv[j]);
+      pv[j] = pv[j] - k.lr * (__fdividef(mh, root(vh) + k.eps) + k.wd * pv[j]);
     }
     if (BITS8) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j >= n) m[j] = v[j] = 0.f;  // behind the tensor's end
-      const float ms = block_top(m), vs = block_top(v);
-      const Ratio mr(ms), vr(vs);
-      uint32_t mq[2] = {0, 0}, vq[2] = {0, 0};
+      ms = block_top(m);
+      vs = block_top(v);
+      // 127 sqrt(m / ms) = sqrt(127^2 m / ms), 255 (v / vs)^(1/4) = sqrt(sqrt(255^4 v / vs))
+      const Ratio mr(ms, 127.f * 127.f), vr(vs, 255.f * 255.f * 255.f * 255.f);
+      uint32_t mo[2] = {0, 0}, vo[2] = {0, 0};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int q = static_cast<int>(rintf(127.f * sqrtf(mr(fabsf(m[j])))));
-        const int u = static_cast<int>(rintf(255.f * sqrtf(sqrtf(vr(v[j])))));
-        mq[j >> 2] |= static_cast<uint32_t>((m[j] < 0.f ? -q : q) & 255) << (8 * (j & 3));
-        vq[j >> 2] |= static_cast<uint32_t>(max(u, v[j] > 0.f ? 1 : 0)) << (8 * (j & 3));
+        const int q = min(127, __float2int_rn(root_ftz(mr(fabsf(m[j])))));
+        const int u = min(255, __float2int_rn(root_ftz(root_ftz(vr(v[j])))));
+        mo[j >> 2] |= static_cast<uint32_t>((m[j] < 0.f ? -q : q) & 255) << (8 * (j & 3));
+        vo[j >> 2] |= static_cast<uint32_t>(max(u, v[j] > 0.f ? 1 : 0)) << (8 * (j & 3));
       }
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at) = make_uint2(mq[0], mq[1]);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at) = make_uint2(vq[0], vq[1]);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at) = make_uint2(mo[0], mo[1]);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at) = make_uint2(vo[0], vo[1]);
       if (lane == 0) {
         a.m_scale[a.block0 + b] = ms;
         a.v_scale[a.block0 + b] = vs;
@@ -195,15 +248,12 @@ __global__ void __launch_bounds__(256) adamw_multi_kernel(const __grid_constant_
         }
     }
     if (whole) {
-      store8(p, pv);
+      store8(p + e, pv);
       if (t.pb) store8(t.pb + e, pv);
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) {
-          store_f(p + j, pv[j]);
-          if (t.pb) store_f(t.pb + e + j, pv[j]);
-        }
+      to_strided(sm, lane, pv);
+      store_strided(p + e0, nb, lane, pv);
+      if (t.pb) store_strided(t.pb + e0, nb, lane, pv);
     }
   }
 }
@@ -230,9 +280,9 @@ __global__ void adamw_values_kernel(const uint8_t* __restrict__ m, const uint8_t
 template <typename P, typename G>
 void launch(const AdamArgs& a, bool bits8, unsigned grid, cudaStream_t st) {
   if (bits8)
-    adamw_multi_kernel<P, G, true><<<grid, 256, 0, st>>>(a);
+    adamw_multi_kernel<P, G, true><<<grid, 32 * WARPS, 0, st>>>(a);
   else
-    adamw_multi_kernel<P, G, false><<<grid, 256, 0, st>>>(a);
+    adamw_multi_kernel<P, G, false><<<grid, 32 * WARPS, 0, st>>>(a);
 }
 
 }  // namespace
@@ -262,15 +312,16 @@ cudaError_t adamw_multi_launch(const soup_adamw_tensor* tensors, int count, cons
     a.blocks = 0;
     for (int i = 0; i < a.count; ++i) {
       const soup_adamw_tensor& t = tensors[i0 + i];
-      const uintptr_t all = reinterpret_cast<uintptr_t>(t.p) | reinterpret_cast<uintptr_t>(t.g) |
-                            reinterpret_cast<uintptr_t>(t.p_bf16_copy);
-      a.t[i] = AdamTensor{t.p, t.g, t.p_bf16_copy, t.n, (all & 15u) == 0};
+      const bool aligned = reinterpret_cast<uintptr_t>(t.p) % (p_bf16 ? 16 : 32) == 0 &&
+                           reinterpret_cast<uintptr_t>(t.g) % (g_bf16 ? 16 : 32) == 0 &&
+                           reinterpret_cast<uintptr_t>(t.p_bf16_copy) % 16 == 0;
+      a.t[i] = AdamTensor{t.p, t.g, t.p_bf16_copy, t.n, aligned};
       a.first[i] = a.blocks;
       a.blocks += (t.n + BLOCK - 1) / BLOCK;
     }
     block0 += a.blocks;
     if (a.blocks == 0) continue;
-    const long long want = (a.blocks + 7) / 8;
+    const long long want = (a.blocks + WARPS - 1) / WARPS;
     const unsigned grid = static_cast<unsigned>(std::min<long long>(want, 8ll * device_sm_count()));
     if (p_bf16)
       g_bf16 ? launch<uint16_t, uint16_t>(a, m_scale != nullptr, grid, st) : launch<uint16_t, float>(a, m_scale != nullptr, grid, st);

@@ -2243,7 +2243,7 @@ soup_status soup_adamw_multi(const soup_adamw_tensor* tensors, int count, const 
       return SOUP_ERR_INVALID_ARG;
   }
   if (!any) return SOUP_OK;
-  if (!m || !v || misaligned(m, 16) || misaligned(v, 16) || misaligned(m_scale, 4) || misaligned(v_scale, 4) ||
+  if (!m || !v || misaligned(m, 32) || misaligned(v, 32) || misaligned(m_scale, 4) || misaligned(v_scale, 4) ||
       misaligned(hp, 4))
     return SOUP_ERR_INVALID_ARG;
   return of_launch(adamw_multi_launch(tensors, count, *o, m, v, m_scale, v_scale, hp, static_cast<cudaStream_t>(stream)));
