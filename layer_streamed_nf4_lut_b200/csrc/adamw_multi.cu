@@ -43,6 +43,7 @@ struct AdamArgs {
   const float* hp;
   Hyper k;
   int count;
+  int run;               // blocks of a warp
   long long blocks;      // of this launch
   long long block0;      // state block of this launch's first
   long long first[LAUNCH_TENSORS];  // first block of each tensor, from this launch's first
@@ -82,42 +83,51 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
       make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-__device__ __forceinline__ float m_value(int q, float scale) {
-  const float r = static_cast<float>(q) * (1.f / 127.f);
-  return r * fabsf(r) * scale;
+// Byte j of a word as a float, and a small whole number as a byte, by way of a float whose last bits are
+// the number: conversions run at an eighth of the rate of these.
+__device__ __forceinline__ float byte_value(uint32_t w, int j, float zero) {  // the byte - zero
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650u | j)) - (8388608.f + zero);
 }
-__device__ __forceinline__ float v_value(int q, float scale) {
-  const float r = static_cast<float>(q) * (1.f / 255.f), r2 = r * r;
-  return r2 * r2 * scale;
+__device__ __forceinline__ uint32_t rounded(float x) { return __float_as_uint(x + 12582912.f); }  // low byte, |x| < 2^21
+__device__ __forceinline__ uint32_t low_bytes(const uint32_t* w) {
+  return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
 }
-// Square root and quotient to about 2^-22: the step they make is lr times a number near 1, and a code
+__device__ __forceinline__ void m_values(uint2 q, float scale, float (&m)[8]) {
+  const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};  // -127 .. 127 as 1 .. 255
+  const float k = scale * (1.f / 16129.f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float r = byte_value(w[j >> 2], j & 3, 128.f);
+    m[j] = r * fabsf(r) * k;
+  }
+}
+__device__ __forceinline__ void v_values(uint2 q, float scale, float (&v)[8]) {
+  const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float r = byte_value(w[j >> 2], j & 3, 0.f), r2 = r * r * (1.f / 65025.f);
+    v[j] = r2 * r2 * scale;
+  }
+}
+// Square root and reciprocal to about 2^-22: the step they make is lr times a number near 1, and a code
 // is 8 bits, while the correctly rounded forms make the 8-bit kernel bound by its arithmetic.
 __device__ __forceinline__ float root(float x) {
-  float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float root_ftz(float x) {
   float y;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// to x / scale for 0 <= x <= scale, also where 1 / scale leaves fp32's range
-struct Ratio {
-  float up, inv;
-  __device__ Ratio(float scale, float to) {
-    up = scale < 1e-25f ? 18446744073709551616.f : 1.f;
-    inv = scale > 0.f ? to / (scale * up) : 0.f;
-  }
-  __device__ float operator()(float x) const { return x * up * inv; }
-};
-// The largest of 256 magnitudes of a warp: non-negative floats order like their bits, and so does a
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The largest of 256 magnitudes of a warp.  Non-negative floats order like their bits, and so does a
 // NaN above every number, which therefore reaches the scale instead of being lost in it.
 __device__ __forceinline__ float block_top(const float (&x)[8]) {
-  unsigned top = 0;
+  float top = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(fabsf(x[j])));
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+  for (int j = 0; j < 8; ++j) asm("max.NaN.f32 %0, %1, %2;" : "=f"(top) : "f"(top), "f"(fabsf(x[j])));
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 }
 
 // A block whose tensor is not aligned for wide accesses, or ends in it: lanes take neighbouring elements
@@ -156,20 +166,24 @@ __global__ void __launch_bounds__(32 * WARPS) adamw_multi_kernel(const __grid_co
   __shared__ __align__(16) float turn[WARPS][BLOCK];
   const int lane = threadIdx.x & 31;
   float* sm = turn[threadIdx.x >> 5];
-  const long long stride = static_cast<long long>(gridDim.x) * WARPS;
   Hyper k = a.k;
   if (a.hp) {
     k.lr = a.hp[0];
     k.bc1 = a.hp[1];
     k.bc2 = a.hp[2];
   }
+  k.bc2 *= 0x1p24f;
   int i = 0;  // the tensor of block b
-  // blocks that are worked at one time lie side by side, which keeps DRAM pages open
-  for (long long b = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); b < a.blocks; b += stride) {
+  // A thread block takes a.run x WARPS neighbouring blocks, its warps side by side: what is in flight at
+  // one time lies together, which keeps DRAM pages open, and the tensor is looked up once a run.
+  const long long b0 = static_cast<long long>(blockIdx.x) * a.run * WARPS + (threadIdx.x >> 5);
+  for (int step = 0; step < a.run; ++step) {
+    const long long b = b0 + step * WARPS;
+    if (b >= a.blocks) return;
     if (i + 1 < a.count && a.first[i + 1] <= b)
 #pragma unroll 1
-      for (int step = 512; step > 0; step >>= 1)
-        if (i + step < a.count && a.first[i + step] <= b) i += step;
+      for (int by = 512; by > 0; by >>= 1)
+        if (i + by < a.count && a.first[i + by] <= b) i += by;
     const AdamTensor& t = a.t[i];
     const long long e0 = (b - a.first[i]) * BLOCK, e = e0 + lane * 8;
     const int nb = static_cast<int>(min(static_cast<long long>(BLOCK), t.n - e0));  // elements of this block, > 0
@@ -200,42 +214,53 @@ __global__ void __launch_bounds__(32 * WARPS) adamw_multi_kernel(const __grid_co
       to_own(sm, lane, gv);
     }
     if (BITS8) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t mw = (j < 4 ? mq.x : mq.y) >> (8 * (j & 3)), vw = (j < 4 ? vq.x : vq.y) >> (8 * (j & 3));
-        m[j] = m_value(static_cast<int8_t>(mw & 255u), ms);
-        v[j] = v_value(static_cast<int>(vw & 255u), vs);
-      }
+      m_values(mq, ms, m);
+      v_values(vq, vs, v);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       m[j] = k.b1 * m[j] + k.g1 * gv[j];
       v[j] = k.b2 * v[j] + k.g2 * gv[j] * gv[j];
-      const float mh = m[j] * k.bc1, vh = v[j] * k.bc2;
-      pv[j] = pv[j] - k.lr * (__fdividef(mh, root(vh) + k.eps) + k.wd * pv[j]);
+      // bc2 carries 2^24: the root takes no subnormal numbers
+      const float under = root(v[j] * k.bc2) * 0x1p-12f + k.eps;
+      pv[j] = pv[j] - k.lr * (m[j] * k.bc1 * reciprocal(under) + k.wd * pv[j]);
     }
     if (BITS8) {
+      if (nb < BLOCK) {  // nothing behind the tensor's end
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j >= n) m[j] = v[j] = 0.f;  // behind the tensor's end
+        for (int j = 0; j < 8; ++j)
+          if (j >= n) m[j] = v[j] = 0.f;
+      }
       ms = block_top(m);
       vs = block_top(v);
-      // 127 sqrt(m / ms) = sqrt(127^2 m / ms), 255 (v / vs)^(1/4) = sqrt(sqrt(255^4 v / vs))
-      const Ratio mr(ms, 127.f * 127.f), vr(vs, 255.f * 255.f * 255.f * 255.f);
-      uint32_t mo[2] = {0, 0}, vo[2] = {0, 0};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int q = min(127, __float2int_rn(root_ftz(mr(fabsf(m[j])))));
-        const int u = min(255, __float2int_rn(root_ftz(root_ftz(vr(v[j])))));
-        mo[j >> 2] |= static_cast<uint32_t>((m[j] < 0.f ? -q : q) & 255) << (8 * (j & 3));
-        vo[j >> 2] |= static_cast<uint32_t>(max(u, v[j] > 0.f ? 1 : 0)) << (8 * (j & 3));
-      }
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at) = make_uint2(mo[0], mo[1]);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at) = make_uint2(vo[0], vo[1]);
       if (lane == 0) {
         a.m_scale[a.block0 + b] = ms;
         a.v_scale[a.block0 + b] = vs;
       }
+      if (ms < 1e-25f || vs < 1e-25f) {  // keep 1 / scale within fp32's range
+        const float um = ms < 1e-25f ? 0x1p64f : 1.f, uv = vs < 1e-25f ? 0x1p64f : 1.f;
+        ms *= um;
+        vs *= uv;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          m[j] *= um;
+          v[j] *= uv;
+        }
+      }
+      // 127 sqrt(m / ms) = sqrt(127^2 m / ms), 255 (v / vs)^(1/4) = sqrt(sqrt(255^4 v / vs))
+      const float mr = ms > 0.f ? 127.f * 127.f / ms : 0.f, vr = vs > 0.f ? 255.f * 255.f * 255.f * 255.f / vs : 0.f;
+      uint32_t mo[8], vo[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mo[j] = rounded(copysignf(root(fabsf(m[j]) * mr), m[j]));
+        float u = root(root(v[j] * vr));
+        if (v[j] > 0.f) u = fmaxf(u, 1.f);
+        vo[j] = rounded(u);
+      }
+      mq = make_uint2(low_bytes(mo), low_bytes(mo + 4));
+      vq = make_uint2(low_bytes(vo), low_bytes(vo + 4));
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at) = mq;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at) = vq;
     } else if (n == 8) {
       store8(static_cast<float*>(a.m) + at, m);
       store8(static_cast<float*>(a.v) + at, v);
@@ -268,11 +293,8 @@ __global__ void adamw_values_kernel(const uint8_t* __restrict__ m, const uint8_t
   const uint2 mq = *reinterpret_cast<const uint2*>(m + at), vq = *reinterpret_cast<const uint2*>(v + at);
   const float ms = m_scale[b], vs = v_scale[b];
   float mf[8], vf[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    mf[j] = m_value(static_cast<int8_t>(((j < 4 ? mq.x : mq.y) >> (8 * (j & 3))) & 255u), ms);
-    vf[j] = v_value(static_cast<int>(((j < 4 ? vq.x : vq.y) >> (8 * (j & 3))) & 255u), vs);
-  }
+  m_values(mq, ms, mf);
+  v_values(vq, vs, vf);
   store8(mo + at, mf);
   store8(vo + at, vf);
 }
@@ -321,8 +343,11 @@ cudaError_t adamw_multi_launch(const soup_adamw_tensor* tensors, int count, cons
     }
     block0 += a.blocks;
     if (a.blocks == 0) continue;
-    const long long want = (a.blocks + WARPS - 1) / WARPS;
-    const unsigned grid = static_cast<unsigned>(std::min<long long>(want, 8ll * device_sm_count()));
+    // Long runs when there are many: at 655,000 blocks 8 a warp save the look-up in most of them, at
+    // 26,000 one a warp spreads them over all SMs.
+    const long long warps = 8ll * WARPS * device_sm_count();
+    a.run = static_cast<int>(std::max(1ll, std::min<long long>(8, a.blocks / (2 * warps))));
+    const unsigned grid = static_cast<unsigned>((a.blocks + a.run * WARPS - 1) / (a.run * WARPS));
     if (p_bf16)
       g_bf16 ? launch<uint16_t, uint16_t>(a, m_scale != nullptr, grid, st) : launch<uint16_t, float>(a, m_scale != nullptr, grid, st);
     else
