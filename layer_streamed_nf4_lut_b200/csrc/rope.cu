@@ -18,25 +18,45 @@ namespace soup {
 
 namespace {
 
+constexpr int ROPE_BLOCK_ANGLES = 1024;  // of one thread block's tokens
+
 struct RopeArgs {
   const void* x[2];  // q, k
   void* y[2];
   long long ldx[2], ldy[2];  // elements between tokens
   int heads[2];
-  int head_dim, rotary;
+  int head_dim, rotary, T;
+  // rope_vec_kernel: groups of 8 values of a head, heads a token's threads take at one time, tokens of a block
+  int items, rows, tokens;
   const int32_t* positions;
   float grow;
   int back;
   double turns[ROPE_MAX_PAIRS];  // f_i / 2 pi
 };
 
-// 8 values as fp32, whichever type they are stored in
+// cos and sin, times grow, of `count` tokens from t0 on: shared by the tokens' heads
+__device__ __forceinline__ void rope_angles(const RopeArgs& a, long long t0, int count, float* cs, float* sn) {
+  const int half = a.rotary / 2;
+  for (int i = threadIdx.x; i < count * half; i += blockDim.x) {
+    const int tl = i / half;
+    const double turns = static_cast<double>(a.positions[t0 + tl]) * a.turns[i - tl * half];
+    float s, c;
+    sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
+    cs[i] = c * a.grow;
+    sn[i] = (a.back ? -s : s) * a.grow;
+  }
+  __syncthreads();
+}
+
+// 8 values as they are stored, and as fp32
 template <typename E>
 struct Vec8;
 template <>
 struct Vec8<uint16_t> {
-  __device__ static void load(const uint16_t* p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+  uint4 u;
+  __device__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = u; }
+  __device__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -45,97 +65,145 @@ struct Vec8<uint16_t> {
       v[2 * j + 1] = f.y;
     }
   }
-  __device__ static void store(uint16_t* p, const float (&v)[8]) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  }
-  __device__ static float get(const uint16_t* p) { return bf16_to_f32(*p); }
-  __device__ static void put(uint16_t* p, float v) {
-    const __nv_bfloat16 b = __float2bfloat16_rn(v);
-    *p = *reinterpret_cast<const uint16_t*>(&b);
+  __device__ void put(const float (&v)[8]) {
+    u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
 };
 template <>
 struct Vec8<float> {
-  __device__ static void load(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  float4 a, b;
+  __device__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ void get(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
-  __device__ static void store(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  __device__ void put(const float (&v)[8]) {
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
   }
-  __device__ static float get(const float* p) { return *p; }
-  __device__ static void put(float* p, float v) { *p = v; }
 };
 
-// One block per token.  VEC: groups of 8 values (the rotated part and, with rotate-half, its halves
-// are whole groups and every address is aligned), else value by value.
-template <typename E, bool PAIRED, bool VEC>
+// Every address aligned and the rotated part (with rotate-half: its halves) whole groups of 8 values.
+// A thread keeps one group of one token, and with it cos and sin in registers, and takes that group of
+// every rows-th head; the first (usually all) heads' values are on their way while the angles are formed.
+template <typename E>
+constexpr int rope_batch(bool paired) { return (paired ? 8 : 4) / (sizeof(E) / 2); }  // heads a thread loads at one time
+
+template <typename E, bool PAIRED>
+__global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int U = rope_batch<E>(PAIRED), V = PAIRED ? 1 : 2;  // loads of a thread and head
+  __shared__ __align__(16) float cs[ROPE_BLOCK_ANGLES], sn[ROPE_BLOCK_ANGLES];
+  const int per_token = a.items * a.rows, half = a.rotary / 2;
+  const int tl = threadIdx.x / per_token, u = threadIdx.x % per_token, k = u % a.items;
+  const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens, t = t0 + tl;
+  const int tokens = static_cast<int>(min(static_cast<long long>(a.tokens), a.T - t0));
+  const int all = tl < tokens ? a.heads[0] + a.heads[1] : 0;
+  const int turn = PAIRED ? a.rotary / 8 : half / 8;
+  const bool turns = k < turn;
+  const int off = turns ? 8 * k : a.rotary + 8 * (k - turn);
+  Vec8<E> x[U][V];
+  auto place = [&](int hd, const long long (&ld)[2], auto* base0, auto* base1) {
+    return hd < a.heads[0] ? base0 + t * ld[0] + static_cast<long long>(hd) * a.head_dim + off
+                           : base1 + t * ld[1] + static_cast<long long>(hd - a.heads[0]) * a.head_dim + off;
+  };
+  auto fetch = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int hd = h0 + i * a.rows;
+      if (hd >= all) continue;
+      const E* p = place(hd, a.ldx, static_cast<const E*>(a.x[0]), static_cast<const E*>(a.x[1]));
+      x[i][0].load(p);
+      if (!PAIRED && turns) x[i][V - 1].load(p + half);
+    }
+  };
+  int h0 = u / a.items;
+  fetch(h0);
+  rope_angles(a, t0, tokens, cs, sn);
+  float c[PAIRED ? 4 : 8], s[PAIRED ? 4 : 8];
+  if (turns && all > 0) {
+    const int at = tl * half + (PAIRED ? 4 : 8) * k;
+#pragma unroll
+    for (int j = 0; j < (PAIRED ? 4 : 8); ++j) {
+      c[j] = cs[at + j];
+      s[j] = sn[at + j];
+    }
+  }
+  while (h0 < all) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int hd = h0 + i * a.rows;
+      if (hd >= all) continue;
+      E* y = place(hd, a.ldy, static_cast<E*>(a.y[0]), static_cast<E*>(a.y[1]));
+      if (turns) {
+        float p[8], q[8];
+        x[i][0].get(p);
+        if (PAIRED) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            q[2 * j] = p[2 * j] * c[j] - p[2 * j + 1] * s[j];
+            q[2 * j + 1] = p[2 * j + 1] * c[j] + p[2 * j] * s[j];
+          }
+          x[i][0].put(q);
+        } else {
+          float lo[8], hi[8];
+          x[i][V - 1].get(q);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            lo[j] = p[j] * c[j] - q[j] * s[j];
+            hi[j] = q[j] * c[j] + p[j] * s[j];
+          }
+          x[i][0].put(lo);
+          x[i][V - 1].put(hi);
+          x[i][V - 1].store(y + half);
+        }
+      }
+      x[i][0].store(y);
+    }
+    h0 += U * a.rows;
+    fetch(h0);
+  }
+}
+
+__device__ __forceinline__ float value_of(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float value_of(const float* p) { return *p; }
+__device__ __forceinline__ void set_value(uint16_t* p, float v) {
+  const __nv_bfloat16 b = __float2bfloat16_rn(v);
+  *p = *reinterpret_cast<const uint16_t*>(&b);
+}
+__device__ __forceinline__ void set_value(float* p, float v) { *p = v; }
+
+// Any alignment, any sizes: a block a token, value by value.
+template <typename E, bool PAIRED>
 __global__ void rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float cs[ROPE_MAX_PAIRS], sn[ROPE_MAX_PAIRS];
   const long long t = blockIdx.x;
   const int half = a.rotary / 2;
-  const double pos = static_cast<double>(a.positions[t]);
-  for (int i = threadIdx.x; i < half; i += blockDim.x) {
-    const double turns = pos * a.turns[i];
-    float s, c;
-    sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
-    cs[i] = c * a.grow;
-    sn[i] = (a.back ? -s : s) * a.grow;
-  }
-  __syncthreads();
+  rope_angles(a, t, 1, cs, sn);
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     if (a.heads[which] == 0) continue;
     const E* x = static_cast<const E*>(a.x[which]) + t * a.ldx[which];
     E* y = static_cast<E*>(a.y[which]) + t * a.ldy[which];
-    const bool copies = static_cast<const void*>(x) != static_cast<void*>(y);
-    constexpr int W = VEC ? 8 : 1;
-    // work items of a head: its pairs (W first members, or W / 2 neighbouring pairs), then its tail
-    const int turn = PAIRED ? (VEC ? a.rotary / 8 : half) : half / W;
-    const int per_head = turn + (copies ? (a.head_dim - a.rotary) / W : 0);
+    // work items of a head: its pairs, then its tail
+    const int per_head = half + (static_cast<const void*>(x) != static_cast<void*>(y) ? a.head_dim - a.rotary : 0);
     for (int i = threadIdx.x; i < per_head * a.heads[which]; i += blockDim.x) {
       const int hd = i / per_head, k = i % per_head;
-      const E* xh = x + hd * a.head_dim;
-      E* yh = y + hd * a.head_dim;
-      if (k >= turn) {
-        const int c = a.rotary + (k - turn) * W;
-        if (VEC) {
-          float v[8];
-          Vec8<E>::load(xh + c, v);
-          Vec8<E>::store(yh + c, v);
-        } else {
-          yh[c] = xh[c];
-        }
-      } else if (VEC && PAIRED) {
-        float v[8];
-        Vec8<E>::load(xh + 8 * k, v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float p = v[2 * j], q = v[2 * j + 1], c = cs[4 * k + j], s = sn[4 * k + j];
-          v[2 * j] = p * c - q * s;
-          v[2 * j + 1] = q * c + p * s;
-        }
-        Vec8<E>::store(yh + 8 * k, v);
-      } else if (VEC) {
-        float v[8], w[8];
-        Vec8<E>::load(xh + 8 * k, v);
-        Vec8<E>::load(xh + half + 8 * k, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float p = v[j], q = w[j], c = cs[8 * k + j], s = sn[8 * k + j];
-          v[j] = p * c - q * s;
-          w[j] = q * c + p * s;
-        }
-        Vec8<E>::store(yh + 8 * k, v);
-        Vec8<E>::store(yh + half + 8 * k, w);
+      const E* xh = x + static_cast<long long>(hd) * a.head_dim;
+      E* yh = y + static_cast<long long>(hd) * a.head_dim;
+      if (k >= half) {
+        yh[a.rotary + k - half] = xh[a.rotary + k - half];
       } else {
         const int i0 = PAIRED ? 2 * k : k, i1 = PAIRED ? 2 * k + 1 : k + half;
-        const float p = Vec8<E>::get(xh + i0), q = Vec8<E>::get(xh + i1);
-        Vec8<E>::put(yh + i0, p * cs[k] - q * sn[k]);
-        Vec8<E>::put(yh + i1, q * cs[k] + p * sn[k]);
+        const float p = value_of(xh + i0), q = value_of(xh + i1);
+        set_value(yh + i0, p * cs[k] - q * sn[k]);
+        set_value(yh + i1, q * cs[k] + p * sn[k]);
       }
     }
   }
@@ -183,42 +251,56 @@ void rope_frequencies(const soup_rope_config& c, double* freq, double* grow) {
 cudaError_t rope_launch(const RopeCall& c, cudaStream_t st) {
   if (c.T <= 0 || c.heads[0] + c.heads[1] == 0) return cudaSuccess;
   RopeArgs a{};
-  bool vec = c.rotary % (c.interleaved ? 8 : 16) == 0 && c.head_dim % 8 == 0;
   const int size = c.f32 ? 4 : 2;
+  bool vec = c.rotary % (c.interleaved ? 8 : 16) == 0 && c.head_dim % 8 == 0, copies = false;
   for (int w = 0; w < 2; ++w) {
     a.x[w] = c.x[w];
     a.y[w] = c.y[w];
     a.ldx[w] = c.ldx[w];
     a.ldy[w] = c.ldy[w];
     a.heads[w] = c.heads[w];
-    if (c.heads[w] && (((reinterpret_cast<uintptr_t>(c.x[w]) | reinterpret_cast<uintptr_t>(c.y[w])) & 15u) ||
-                       (c.ldx[w] * size) % 16 || (c.ldy[w] * size) % 16))
+    if (!c.heads[w]) continue;
+    if (((reinterpret_cast<uintptr_t>(c.x[w]) | reinterpret_cast<uintptr_t>(c.y[w])) & 15u) ||
+        (c.ldx[w] * size) % 16 || (c.ldy[w] * size) % 16)
       vec = false;
+    copies = copies || c.x[w] != c.y[w];
   }
   a.head_dim = c.head_dim;
   a.rotary = c.rotary;
+  a.T = c.T;
   a.positions = c.positions;
   a.grow = c.grow;
   a.back = c.back;
   for (int i = 0; i < c.rotary / 2; ++i) a.turns[i] = c.freq[i] / 6.283185307179586476925;
-  const int items = (c.heads[0] + c.heads[1]) * c.head_dim / (vec ? 16 : 2);
-  const int threads = std::max(64, std::min(256, (items + 31) / 32 * 32));
-  const dim3 grid(static_cast<unsigned>(c.T));
-#define SOUP_ROPE(E)                                                                          \
-  do {                                                                                        \
-    if (c.interleaved)                                                                        \
-      vec ? rope_kernel<E, true, true><<<grid, threads, 0, st>>>(a)                           \
-          : rope_kernel<E, true, false><<<grid, threads, 0, st>>>(a);                         \
-    else                                                                                      \
-      vec ? rope_kernel<E, false, true><<<grid, threads, 0, st>>>(a)                          \
-          : rope_kernel<E, false, false><<<grid, threads, 0, st>>>(a);                        \
-  } while (0)
-  if (c.f32)
-    SOUP_ROPE(float);
-  else
-    SOUP_ROPE(uint16_t);
-#undef SOUP_ROPE
+  const int heads = c.heads[0] + c.heads[1];
+  a.items = c.rotary / (c.interleaved ? 8 : 16) + (copies ? (c.head_dim - c.rotary) / 8 : 0);
   ++g_kernel_launches;
+  if (vec && a.items <= 256) {
+    // as few rounds over the heads as 256 threads allow, and as many tokens in a block as then fit; one
+    // token where that leaves SMs without a block
+    const int batch = (c.interleaved ? 8 : 4) / (size / 2);
+    int rounds = 1;
+    while (a.items * ((heads + batch * rounds - 1) / (batch * rounds)) > 256) ++rounds;
+    a.rows = (heads + batch * rounds - 1) / (batch * rounds);
+    a.tokens = std::max(1, std::min(256 / (a.items * a.rows), ROPE_BLOCK_ANGLES / (c.rotary / 2)));
+    a.tokens = std::max(1, std::min(a.tokens, c.T / (2 * device_sm_count())));
+    const int threads = (a.tokens * a.items * a.rows + 31) / 32 * 32;
+    const dim3 grid(static_cast<unsigned>((c.T + a.tokens - 1) / a.tokens));
+    if (c.f32)
+      c.interleaved ? rope_vec_kernel<float, true><<<grid, threads, 0, st>>>(a)
+                    : rope_vec_kernel<float, false><<<grid, threads, 0, st>>>(a);
+    else
+      c.interleaved ? rope_vec_kernel<uint16_t, true><<<grid, threads, 0, st>>>(a)
+                    : rope_vec_kernel<uint16_t, false><<<grid, threads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  const dim3 grid(static_cast<unsigned>(c.T));
+  const int threads = static_cast<int>(std::max(64ll, std::min(256ll, (1ll * heads * c.head_dim / 2 + 31) / 32 * 32)));
+  if (c.f32)
+    c.interleaved ? rope_kernel<float, true><<<grid, threads, 0, st>>>(a) : rope_kernel<float, false><<<grid, threads, 0, st>>>(a);
+  else
+    c.interleaved ? rope_kernel<uint16_t, true><<<grid, threads, 0, st>>>(a)
+                  : rope_kernel<uint16_t, false><<<grid, threads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
