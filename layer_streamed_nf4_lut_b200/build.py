@@ -1,4 +1,5 @@
-"""Builds libsoup.so (all CUDA sources, sm_100a) next to this file.
+"""Builds libsoup.so (all CUDA sources, sm_100a) and _torch_calls.so (the operators' calls on torch
+tensors, host C++) next to this file.
 
 Usage: python -m layer_streamed_nf4_lut_b200.build [--verbose]
 """
@@ -13,7 +14,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsoup.so")
+CALLS = os.path.join(HERE, "_torch_calls.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CXX = os.environ.get("CXX", "g++")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O3",
          "-I" + os.path.join(ROOT, "include")]
@@ -24,12 +27,39 @@ def sources():
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+        glob.glob(os.path.join(CSRC, "*.cpp")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _compile_calls(obj: str, verbose: bool):
+    import sysconfig
+    from importlib.util import find_spec
+    src = os.path.join(CSRC, "torch_calls.cpp")
+    torch_dir = os.path.dirname(find_spec("torch").origin)
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+           os.path.join(ROOT, "include")]
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", *("-I" + d for d in inc), "-c", src, "-o", obj]
+    if verbose:
+        print(" ".join(cmd))
+    return src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _link_calls(obj: str, verbose: bool):
+    from importlib.util import find_spec
+    torch_lib = os.path.join(os.path.dirname(find_spec("torch").origin), "lib")
+    # libsoup.so is found beside it, whatever the tree's place
+    cmd = [CXX, "-shared", obj, "-o", CALLS + ".tmp", "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-L" + HERE, "-l:libsoup.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    os.replace(CALLS + ".tmp", CALLS)
 
 
 def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) -> str:
@@ -38,7 +68,8 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     objs = []
-    procs = []
+    calls_obj = os.path.join(objdir, "torch_calls.cpp.o")
+    procs = [_compile_calls(calls_obj, verbose)]
     for src in sources():
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
         cmd = [NVCC, *ARCH, *FLAGS, "-c", src, "-o", obj]
@@ -56,13 +87,14 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError("nvcc failed for: " + ", ".join(failed))
+        raise RuntimeError("the compiler failed for: " + ", ".join(failed))
     tmp = LIB + ".tmp"
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    _link_calls(calls_obj, verbose)
     return LIB
 
 

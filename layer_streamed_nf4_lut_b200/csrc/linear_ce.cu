@@ -25,6 +25,7 @@
 #include "tc.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 namespace soup {
@@ -718,9 +719,16 @@ cudaError_t launch(void (*kernel)(Params...), int grid, int threads, int smem, c
 }
 
 cudaError_t gemm_attributes() {
-  // per device and cheap, so set before each call: two function attributes
+  // once for each device; setting them twice at the same time does no harm
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  CE_CK(cudaGetDevice(&dev));
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load() & bit) return cudaSuccess;
   CE_CK(cudaFuncSetAttribute(ce_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
-  return cudaFuncSetAttribute(ce_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  CE_CK(cudaFuncSetAttribute(ce_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
+  done.fetch_or(bit);
+  return cudaSuccess;
 }
 
 }  // namespace

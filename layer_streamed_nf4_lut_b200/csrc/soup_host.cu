@@ -2298,8 +2298,17 @@ soup_status soup_rope(const soup_rope_config* cfg, const void* q, long long ldq,
     c.ldy[i] = ldy[i];
     c.heads[i] = heads[i];
   }
-  double freq[ROPE_MAX_PAIRS], grow;
-  rope_frequencies(*cfg, freq, &grow);
+  // a token's call is shorter than the frequencies' powers: the last configuration's are kept
+  static thread_local struct {
+    soup_rope_config cfg;
+    double freq[ROPE_MAX_PAIRS], grow;
+  } last = {};
+  if (std::memcmp(&last.cfg, cfg, sizeof(*cfg)) != 0) {
+    rope_frequencies(*cfg, last.freq, &last.grow);
+    last.cfg = *cfg;
+  }
+  const double* freq = last.freq;
+  const double grow = last.grow;
   c.head_dim = head_dim;
   c.rotary = cfg->rotary_dim;
   c.T = T;

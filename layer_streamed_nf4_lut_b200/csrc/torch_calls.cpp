@@ -1,0 +1,329 @@
+// The calls of model.py's operators on torch tensors, from argument checks to the C-ABI.  Marshalling only, as the
+// ctypes binding does it for the rest of the library; in C++ because a step calls these on hundreds of
+// small tensors and for single tokens, where checks from Python took longer than the kernels (rope
+// of one token: 27 us a call, 3 of them the kernel; AdamW over 448 tensors: 424 us).
+#include <Python.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+
+#include <cstring>
+#include <vector>
+
+#include "soup.h"
+
+namespace {
+
+PyObject* soup_error = nullptr;  // _lib.SoupError(status, message)
+
+struct Refused {  // the Python error is set
+};
+
+[[noreturn]] void fail(int status, const char* why) {
+  PyObject* e = PyObject_CallFunction(soup_error, "is", status, why);
+  if (e) {
+    PyErr_SetObject(soup_error, e);
+    Py_DECREF(e);
+  }
+  throw Refused{};
+}
+void need(bool ok, const char* why) {
+  if (!ok) fail(SOUP_ERR_INVALID_ARG, why);
+}
+void check(soup_status s) {
+  if (s != SOUP_OK) fail(s, soup_status_string(s));
+}
+
+const at::Tensor& tensor(PyObject* o, const char* why) {
+  need(o && THPVariable_Check(o), why);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  need(t.layout() == at::kStrided && t.is_cuda(), why);
+  return t;
+}
+// None: an undefined tensor
+at::Tensor maybe_tensor(PyObject* o, const char* why) { return o == Py_None ? at::Tensor() : tensor(o, why); }
+void* ptr(const at::Tensor& t) { return t.defined() ? const_cast<void*>(t.const_data_ptr()) : nullptr; }
+PyObject* wrap(at::Tensor t) {
+  PyObject* o = THPVariable_Wrap(std::move(t));
+  if (!o) throw Refused{};
+  return o;
+}
+void* stream_of(const at::Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Refused{};
+  return v;
+}
+long long whole(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Refused{};
+  return v;
+}
+
+struct Owned {  // a reference that is let go with the scope
+  PyObject* o;
+  explicit Owned(PyObject* p) : o(p) {
+    if (!p) throw Refused{};
+  }
+  Owned(const Owned&) = delete;
+  ~Owned() { Py_XDECREF(o); }
+  PyObject* give() {
+    PyObject* p = o;
+    o = nullptr;
+    return p;
+  }
+};
+struct Unlocked {  // other Python threads run while the library launches
+  PyThreadState* s = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(s); }
+};
+#define UNLOCKED(call) ([&] { Unlocked u; return (call); }())
+
+// ---------------------------------------------------------------- loss over the vocabulary
+struct Sizes {
+  int T, H, V;
+};
+Sizes loss_sizes(const at::Tensor& h, const at::Tensor& w) {
+  need(h.dim() == 2 && w.dim() == 2 && h.size(1) == w.size(1), "linear_ce: h [T, hidden] and w [vocab, hidden]");
+  need(h.scalar_type() == at::kBFloat16 && w.scalar_type() == at::kBFloat16 && w.device() == h.device(),
+       "linear_ce: h and w are bf16 tensors of one GPU");
+  need(h.size(1) <= 1 || (h.stride(1) == 1 && w.stride(1) == 1), "linear_ce: rows of h and w are contiguous");
+  need(h.size(0) < INT_MAX && h.size(1) < INT_MAX && w.size(0) < INT_MAX, "linear_ce: sizes below 2^31");
+  return {static_cast<int>(h.size(0)), static_cast<int>(h.size(1)), static_cast<int>(w.size(0))};
+}
+void row_values(const at::Tensor& t, at::ScalarType type, int T, const at::Tensor& like, const char* why) {
+  need(!t.defined() || (t.scalar_type() == type && t.dim() == 1 && t.size(0) == T && t.is_contiguous() &&
+                        t.device() == like.device()),
+       why);
+}
+constexpr const char* GPU_TENSORS = "linear_ce: tensors on a GPU";
+
+struct Forward {
+  at::Tensor ws, lse, logp, logp2;
+};
+Forward loss_forward(const at::Tensor& h, const at::Tensor& w, const Sizes& n, const at::Tensor& t1, const at::Tensor& t2,
+                     bool grad, bool check_targets) {
+  size_t bytes = 0;
+  check(soup_linear_ce_workspace(n.T, n.H, n.V, grad, &bytes));
+  Forward f;
+  f.ws = at::empty({static_cast<int64_t>(bytes)}, h.options().dtype(at::kByte));
+  const at::Tensor res = at::empty({t2.defined() ? 3 : 2, n.T}, h.options().dtype(at::kFloat));
+  f.lse = res.select(0, 0);
+  f.logp = res.select(0, 1);
+  if (t2.defined()) f.logp2 = res.select(0, 2);
+  at::Tensor err;
+  if (check_targets) err = at::zeros({1}, h.options().dtype(at::kInt));
+  void* st = stream_of(h);
+  check(UNLOCKED(soup_linear_ce_fwd(ptr(h), n.T > 1 ? h.stride(0) : n.H, ptr(w), n.V > 1 ? w.stride(0) : n.H, n.T, n.H, n.V,
+                                    static_cast<int32_t*>(ptr(t1)), static_cast<int32_t*>(ptr(t2)), grad,
+                                    static_cast<float*>(ptr(f.lse)), static_cast<float*>(ptr(f.logp)),
+                                    static_cast<float*>(ptr(f.logp2)), ptr(f.ws), bytes, static_cast<int*>(ptr(err)), st)));
+  if (err.defined()) {
+    const int bad = UNLOCKED(err.item<int>());
+    if (bad) fail(SOUP_ERR_DEVICE_CHECK, "linear_ce: a target is not below the vocabulary's size");
+  }
+  return f;
+}
+at::Tensor loss_backward(const at::Tensor& w, const Sizes& n, const at::Tensor& ws, const at::Tensor& weight,
+                         const at::Tensor& weight2) {
+  at::Tensor dh = at::empty({n.T, n.H}, w.options());
+  void* st = stream_of(w);
+  check(UNLOCKED(soup_linear_ce_bwd(ptr(w), n.V > 1 ? w.stride(0) : n.H, n.T, n.H, n.V, static_cast<float*>(ptr(weight)),
+                                    static_cast<float*>(ptr(weight2)), ptr(dh), n.H, ptr(ws), ws.nbytes(), st)));
+  return dh;
+}
+void put(PyObject* dict, const char* key, at::Tensor t) {
+  Owned o(wrap(std::move(t)));
+  if (PyDict_SetItemString(dict, key, o.o) < 0) throw Refused{};
+}
+
+// linear_ce(h, w, targets, weight, targets2, weight2, check_targets, saved) -> dict
+PyObject* linear_ce(PyObject* const* a) {
+  const at::Tensor h = tensor(a[0], GPU_TENSORS), w = tensor(a[1], GPU_TENSORS);
+  const at::Tensor t1 = tensor(a[2], GPU_TENSORS), weight = maybe_tensor(a[3], GPU_TENSORS);
+  const at::Tensor t2 = maybe_tensor(a[4], GPU_TENSORS), weight2 = maybe_tensor(a[5], GPU_TENSORS);
+  const bool check_targets = PyObject_IsTrue(a[6]), keep = PyObject_IsTrue(a[7]);
+  const Sizes n = loss_sizes(h, w);
+  const char* why = "linear_ce: targets are contiguous int32 [T] on the device of h";
+  row_values(t1, at::kInt, n.T, h, why);
+  row_values(t2, at::kInt, n.T, h, why);
+  why = "linear_ce: weights are contiguous fp32 [T] on the device of w";
+  row_values(weight, at::kFloat, n.T, h, why);
+  row_values(weight2, at::kFloat, n.T, h, why);
+  need(weight.defined() || !weight2.defined(), "linear_ce: weight2 goes with weight");
+  const c10::cuda::CUDAGuard guard(h.device());
+  Forward f = loss_forward(h, w, n, t1, t2, keep || weight.defined(), check_targets);
+  Owned out(PyDict_New());
+  put(out.o, "lse", f.lse);
+  put(out.o, "logp", f.logp);
+  if (keep) {
+    Owned ws(wrap(f.ws));
+    Owned saved(Py_BuildValue("(Oiii)", ws.o, n.T, n.H, n.V));
+    if (PyDict_SetItemString(out.o, "saved", saved.o) < 0) throw Refused{};
+  }
+  if (t2.defined()) put(out.o, "logp2", f.logp2);
+  if (weight.defined()) put(out.o, "dh", loss_backward(w, n, f.ws, weight, weight2));
+  return out.give();
+}
+
+// linear_ce_bwd(w, saved, weight, weight2) -> dh
+PyObject* linear_ce_bwd(PyObject* const* a) {
+  const at::Tensor w = tensor(a[0], GPU_TENSORS), weight = tensor(a[2], GPU_TENSORS), weight2 = maybe_tensor(a[3], GPU_TENSORS);
+  PyObject* ws_obj = nullptr;
+  Sizes n{};
+  need(PyTuple_Check(a[1]), "linear_ce: \"saved\" of a forward call with grad");
+  if (!PyArg_ParseTuple(a[1], "Oiii", &ws_obj, &n.T, &n.H, &n.V)) throw Refused{};
+  const at::Tensor ws = tensor(ws_obj, GPU_TENSORS);
+  need(w.dim() == 2 && w.size(1) == n.H && w.size(0) == n.V && w.scalar_type() == at::kBFloat16 &&
+           (n.H <= 1 || w.stride(1) == 1) && ws.device() == w.device() && ws.is_contiguous(),
+       "linear_ce: the w of the forward call");
+  const char* why = "linear_ce: weights are contiguous fp32 [T] on the device of w";
+  row_values(weight, at::kFloat, n.T, w, why);
+  row_values(weight2, at::kFloat, n.T, w, why);
+  const c10::cuda::CUDAGuard guard(w.device());
+  return wrap(loss_backward(w, n, ws, weight, weight2));
+}
+
+// ---------------------------------------------------------------- AdamW
+// adamw_multi(params, grads, m, v, m_scale, v_scale, hp, lr, step, beta1, beta2, eps, weight_decay)
+PyObject* adamw_multi(PyObject* const* a) {
+  Owned ps(PySequence_Fast(a[0], "adamw: params is a sequence")), gs(PySequence_Fast(a[1], "adamw: grads is a sequence"));
+  const Py_ssize_t count = PySequence_Fast_GET_SIZE(ps.o);
+  need(PySequence_Fast_GET_SIZE(gs.o) == count, "adamw: as many gradients as parameters");
+  if (count == 0) Py_RETURN_NONE;
+  need(count < INT_MAX, "adamw: fewer than 2^31 tensors");
+  const char* why = "adamw: states of adamw_state(sizes) for these parameters";
+  const at::Tensor m = tensor(a[2], why), v = tensor(a[3], why), ms = maybe_tensor(a[4], why), vs = maybe_tensor(a[5], why);
+  const at::Tensor hp = maybe_tensor(a[6], "adamw: hp is fp32 [3] on the device of the states");
+  const c10::Device dev = m.device();
+  const char* each = "adamw: contiguous tensors of one type and device, each gradient of its parameter's size";
+  at::ScalarType pt = at::kFloat, gt = at::kFloat;
+  std::vector<soup_adamw_tensor> table(static_cast<size_t>(count));
+  long long blocks = 0;
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    PyObject* po = PySequence_Fast_GET_ITEM(ps.o, i);
+    PyObject* go = PySequence_Fast_GET_ITEM(gs.o, i);
+    const at::Tensor &p = tensor(po, each), &g = tensor(go, each);
+    if (i == 0) {
+      pt = p.scalar_type();
+      gt = g.scalar_type();
+      need((pt == at::kFloat || pt == at::kBFloat16) && (gt == at::kFloat || gt == at::kBFloat16), "adamw: fp32 or bf16 tensors");
+    }
+    need(p.scalar_type() == pt && g.scalar_type() == gt && p.numel() == g.numel() && p.device() == dev && g.device() == dev &&
+             p.is_contiguous() && g.is_contiguous(),
+         each);
+    table[static_cast<size_t>(i)] = soup_adamw_tensor{ptr(p), ptr(g), nullptr, p.numel()};
+    blocks += (p.numel() + SOUP_ADAMW_BLOCK - 1) / SOUP_ADAMW_BLOCK;
+  }
+  const bool bits8 = ms.defined();
+  need(m.numel() == blocks * SOUP_ADAMW_BLOCK && v.numel() == m.numel() && v.device() == dev && m.is_contiguous() &&
+           v.is_contiguous() && vs.defined() == bits8,
+       why);
+  if (bits8)
+    need(m.scalar_type() == at::kChar && v.scalar_type() == at::kByte && ms.scalar_type() == at::kFloat &&
+             vs.scalar_type() == at::kFloat && ms.numel() == blocks && vs.numel() == blocks && ms.is_contiguous() &&
+             vs.is_contiguous() && ms.device() == dev && vs.device() == dev,
+         "adamw: int8 m, uint8 v and an fp32 scale for each block");
+  else
+    need(m.scalar_type() == at::kFloat && v.scalar_type() == at::kFloat, "adamw: fp32 states, or 8-bit ones with their scales");
+  need(!hp.defined() || (hp.scalar_type() == at::kFloat && hp.numel() >= 3 && hp.device() == dev && hp.is_contiguous()),
+       "adamw: hp is fp32 [3] on the device of the states");
+  const long long step = whole(a[8]);
+  need(step <= INT_MAX && step >= INT_MIN, "adamw: step below 2^31");
+  const soup_adamw_options o{pt == at::kBFloat16, gt == at::kBFloat16, static_cast<int>(step), number(a[7]), number(a[9]),
+                             number(a[10]), number(a[11]), number(a[12])};
+  const c10::cuda::CUDAGuard guard(dev);
+  void* st = stream_of(m);
+  check(UNLOCKED(soup_adamw_multi(table.data(), static_cast<int>(count), &o, ptr(m), ptr(v), static_cast<float*>(ptr(ms)),
+                                  static_cast<float*>(ptr(vs)), static_cast<float*>(ptr(hp)), st)));
+  Py_RETURN_NONE;
+}
+
+// adamw_state_values(m, v, m_scale, v_scale) -> (m, v) in bf16
+PyObject* adamw_state_values(PyObject* const* a) {
+  const char* why = "adamw: 8-bit states and their scales";
+  const at::Tensor m = tensor(a[0], why), v = tensor(a[1], why), ms = tensor(a[2], why), vs = tensor(a[3], why);
+  need(m.scalar_type() == at::kChar && v.scalar_type() == at::kByte && ms.scalar_type() == at::kFloat &&
+           vs.scalar_type() == at::kFloat && m.numel() == SOUP_ADAMW_BLOCK * ms.numel() && v.numel() == m.numel() &&
+           vs.numel() == ms.numel() && v.device() == m.device() && ms.device() == m.device() && vs.device() == m.device() &&
+           m.is_contiguous() && v.is_contiguous() && ms.is_contiguous() && vs.is_contiguous(),
+       why);
+  const c10::cuda::CUDAGuard guard(m.device());
+  at::Tensor mo = at::empty(m.sizes(), m.options().dtype(at::kBFloat16)), vo = at::empty(v.sizes(), mo.options());
+  void* st = stream_of(m);
+  check(UNLOCKED(soup_adamw_state_values(ptr(m), ptr(v), static_cast<float*>(ptr(ms)), static_cast<float*>(ptr(vs)), m.numel(),
+                                         static_cast<uint16_t*>(ptr(mo)), static_cast<uint16_t*>(ptr(vo)), st)));
+  Owned x(wrap(mo)), y(wrap(vo));
+  return PyTuple_Pack(2, x.o, y.o);
+}
+
+// ---------------------------------------------------------------- rotary positions
+// rope(config as bytes, q, k, positions, inverse, inplace) -> (q, k)
+PyObject* rope(PyObject* const* a) {
+  soup_rope_config cfg;
+  need(PyBytes_Check(a[0]) && PyBytes_GET_SIZE(a[0]) == sizeof(cfg), "rope: a soup_rope_config");
+  std::memcpy(&cfg, PyBytes_AS_STRING(a[0]), sizeof(cfg));
+  const char* why = "rope: bf16 or fp32 q on a GPU and contiguous int32 positions [T] beside it";
+  const char* form = "rope: [T, heads, d] with contiguous heads, k like q";
+  const at::Tensor q = tensor(a[1], why), k = maybe_tensor(a[2], form), pos = tensor(a[3], why);
+  const bool inverse = PyObject_IsTrue(a[4]), inplace = PyObject_IsTrue(a[5]);
+  need(q.dim() == 3, form);
+  const int64_t T = q.size(0), d = q.size(2);
+  need((q.scalar_type() == at::kBFloat16 || q.scalar_type() == at::kFloat) && pos.scalar_type() == at::kInt && pos.dim() == 1 &&
+           pos.size(0) == T && pos.device() == q.device() && pos.is_contiguous(),
+       why);
+  for (const at::Tensor* x : {&q, &k})
+    need(!x->defined() || (x->dim() == 3 && x->size(0) == T && x->size(2) == d && x->scalar_type() == q.scalar_type() &&
+                           x->device() == q.device() && (x->stride(2) == 1 || d == 1) && (x->stride(1) == d || x->size(1) == 1)),
+         form);
+  need(T < INT_MAX && d < INT_MAX && q.size(1) < INT_MAX && (!k.defined() || k.size(1) < INT_MAX), "rope: sizes below 2^31");
+  const c10::cuda::CUDAGuard guard(q.device());
+  const at::Tensor qo = inplace ? q : at::empty(q.sizes(), q.options());
+  const at::Tensor ko = inplace || !k.defined() ? k : at::empty(k.sizes(), k.options());
+  void* st = stream_of(q);
+  check(UNLOCKED(soup_rope(&cfg, ptr(q), q.stride(0), ptr(qo), qo.stride(0), static_cast<int>(q.size(1)), ptr(k),
+                           k.defined() ? k.stride(0) : 0, ptr(ko), ko.defined() ? ko.stride(0) : 0,
+                           k.defined() ? static_cast<int>(k.size(1)) : 0, static_cast<int>(d), static_cast<int>(T),
+                           static_cast<int32_t*>(ptr(pos)), q.scalar_type() == at::kFloat, inverse, st)));
+  if (inplace) return PyTuple_Pack(2, a[1], a[2]);
+  Owned x(wrap(qo));
+  if (!k.defined()) return PyTuple_Pack(2, x.o, Py_None);
+  Owned y(wrap(ko));
+  return PyTuple_Pack(2, x.o, y.o);
+}
+
+// ---------------------------------------------------------------- the module
+template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
+PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != N) {
+    PyErr_Format(PyExc_TypeError, "%zd arguments are needed", N);
+    return nullptr;
+  }
+  try {
+    return F(args);
+  } catch (const Refused&) {
+  } catch (const std::exception& e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "an unknown exception");
+  }
+  return nullptr;
+}
+PyObject* set_error(PyObject*, PyObject* type) {
+  Py_XINCREF(type);
+  Py_XDECREF(soup_error);
+  soup_error = type;
+  Py_RETURN_NONE;
+}
+#define METHOD(name, n) \
+  { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&call<name, n>)), METH_FASTCALL, nullptr }
+PyMethodDef methods[] = {METHOD(linear_ce, 8),          METHOD(linear_ce_bwd, 4), METHOD(adamw_multi, 13),
+                         METHOD(adamw_state_values, 4), METHOD(rope, 6),          {"set_error", set_error, METH_O, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__torch_calls() { return PyModule_Create(&module_def); }

@@ -4,15 +4,17 @@ step of the computation runs in libsoup's CUDA kernels.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from ctypes import byref, c_float, c_int, c_size_t, c_void_p
 
 import numpy as np
 import torch
 
-from . import _lib
+from . import _lib, _torch_calls as _calls
 from ._lib import PROJ, Batch, ModelConfig, SoupError, Stats, check, lib
+
+_calls.set_error(SoupError)
 
 
 def make_config(cfg: dict, mode: str = "streamed", n_layer_buffers: int = 2, max_tokens: int | None = None,
@@ -386,11 +388,6 @@ def nf4_matmul(x: torch.Tensor, q: dict, transpose_w: bool = False, residual: to
     return y
 
 
-def _on_device(t: torch.Tensor):
-    """Makes t's device the current one for a call (the library launches on the current device)."""
-    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
-
-
 def _need(ok: bool, why: str):
     if not ok:
         raise SoupError(-1, why)
@@ -404,57 +401,19 @@ def linear_ce(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, weight: t
     Returns fp32 [T] "lse" and "logp" (and "logp2" with targets2).  With weight (fp32 [T]; weight2
     for targets2), also "dh" bf16: the gradient of -sum(weight logp + weight2 logp2) with respect
     to h.  check_targets reads the bounds check back (synchronises) and raises on a target >= vocab."""
-    out = linear_ce_fwd(h, w, targets, targets2, grad=weight is not None, check_targets=check_targets)
-    saved = out.pop("saved")
-    if weight is not None:
-        out["dh"] = linear_ce_bwd(w, saved, weight, weight2)
-    return out
+    return _calls.linear_ce(h, w, targets, weight, targets2, weight2, check_targets, False)
 
 
 def linear_ce_fwd(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, targets2: torch.Tensor | None = None,
                   grad: bool = True, check_targets: bool = False) -> dict:
     """The forward half of linear_ce: "saved" of the result goes to linear_ce_bwd, for weights that
-    depend on the log-probs (the preference losses)."""
-    _need(h.dim() == 2 and w.dim() == 2 and h.shape[1] == w.shape[1], "linear_ce: h [T, hidden] and w [vocab, hidden]")
-    _need(h.is_cuda and h.dtype == torch.bfloat16 and w.dtype == torch.bfloat16 and w.device == h.device,
-          "linear_ce: h and w are bf16 tensors of one GPU")
-    T, H = h.shape
-    for t in (targets, targets2):
-        _need(t is None or (t.dtype == torch.int32 and t.shape == (T,) and t.is_contiguous() and t.device == h.device),
-              "linear_ce: targets are contiguous int32 [T] on the device of h")
-    _need((H <= 1 or (h.stride(1) == 1 and w.stride(1) == 1)), "linear_ce: rows of h and w are contiguous")
-    with _on_device(h):
-        n = c_size_t()
-        check(lib.soup_linear_ce_workspace(T, H, w.shape[0], 1 if grad else 0, byref(n)))
-        ws = torch.empty(n.value, dtype=torch.uint8, device=h.device)
-        res = torch.empty((2 if targets2 is None else 3, T), dtype=torch.float32, device=h.device)
-        err = torch.zeros(1, dtype=torch.int32, device=h.device) if check_targets else None
-        check(lib.soup_linear_ce_fwd(h.data_ptr(), h.stride(0) if T > 1 else H, w.data_ptr(),
-                                     w.stride(0) if w.shape[0] > 1 else H, T, H, w.shape[0], targets.data_ptr(),
-                                     _ptr(targets2), 1 if grad else 0, res[0].data_ptr(), res[1].data_ptr(),
-                                     None if targets2 is None else res[2].data_ptr(), ws.data_ptr(), n.value, _ptr(err),
-                                     _stream_ptr()))
-        if err is not None and int(err.item()) != 0:
-            raise SoupError(-6, "linear_ce: a target is not below the vocabulary's size")
-    out = {"lse": res[0], "logp": res[1], "saved": (ws, T)}
-    if targets2 is not None:
-        out["logp2"] = res[2]
-    return out
+    depend on the log-probs (the preference losses); without grad there is none."""
+    return _calls.linear_ce(h, w, targets, None, targets2, None, check_targets, grad)
 
 
 def linear_ce_bwd(w: torch.Tensor, saved, weight: torch.Tensor, weight2: torch.Tensor | None = None) -> torch.Tensor:
     """dh (bf16 [T, hidden]) of a linear_ce_fwd(..., grad=True) call with the same w."""
-    ws, T = saved
-    for t in (weight, weight2):
-        _need(t is None or (t.dtype == torch.float32 and t.shape == (T,) and t.is_contiguous() and t.device == w.device),
-              "linear_ce: weights are contiguous fp32 [T] on the device of w")
-    H = w.shape[1]
-    with _on_device(w):
-        dh = torch.empty((T, H), dtype=torch.bfloat16, device=w.device)
-        check(lib.soup_linear_ce_bwd(w.data_ptr(), w.stride(0) if w.shape[0] > 1 else H, T, H, w.shape[0],
-                                     weight.data_ptr(), _ptr(weight2), dh.data_ptr(), H, ws.data_ptr(), ws.numel(),
-                                     _stream_ptr()))
-    return dh
+    return _calls.linear_ce_bwd(w, saved, weight, weight2)
 
 
 def adamw_state(sizes, bits: int = 8, device="cuda") -> dict:
@@ -475,50 +434,12 @@ def adamw_multi(params, grads, m: torch.Tensor, v: torch.Tensor, lr: float, step
     """AdamW on every tensor of params (contiguous, all fp32 or all bf16) from grads, in place, in one
     launch; m and v as adamw_state lays them out, 8-bit when the scales are given.  hp: fp32 [3] on the
     device with lr, 1/(1-b1^step), 1/(1-b2^step), read in place of lr and step."""
-    n = len(params)
-    _need(len(grads) == n, "adamw: as many gradients as parameters")
-    if n == 0:
-        return
-    p0, g0, dev = params[0].dtype, grads[0].dtype, m.device
-    _need(p0 in (torch.float32, torch.bfloat16) and g0 in (torch.float32, torch.bfloat16), "adamw: fp32 or bf16 tensors")
-    rows, blocks = [], 0
-    for p, g in zip(params, grads):
-        k = p.numel()
-        if p.dtype != p0 or g.dtype != g0 or g.numel() != k or p.device != dev or g.device != dev or \
-                not p.is_contiguous() or not g.is_contiguous():
-            raise SoupError(-1, "adamw: contiguous tensors of one type and device, each gradient of its parameter's size")
-        blocks += (k + 255) >> 8
-        rows.append((p.data_ptr(), g.data_ptr(), 0, k))
-    bits8 = m_scale is not None
-    _need(m.numel() == blocks * 256 and v.numel() == m.numel() and m.is_cuda and v.device == dev and
-          m.is_contiguous() and v.is_contiguous() and (v_scale is not None) == bits8,
-          "adamw: states of adamw_state(sizes) for these parameters")
-    if bits8:
-        _need(m.dtype == torch.int8 and v.dtype == torch.uint8 and m_scale.dtype == v_scale.dtype == torch.float32 and
-              m_scale.numel() == v_scale.numel() == blocks and m_scale.is_contiguous() and v_scale.is_contiguous() and
-              m_scale.device == dev and v_scale.device == dev, "adamw: int8 m, uint8 v and an fp32 scale for each block")
-    else:
-        _need(m.dtype == torch.float32 and v.dtype == torch.float32, "adamw: fp32 states, or 8-bit ones with their scales")
-    _need(hp is None or (hp.dtype == torch.float32 and hp.numel() >= 3 and hp.device == dev and hp.is_contiguous()),
-          "adamw: hp is fp32 [3] on the device of the states")
-    table = np.array(rows, dtype=np.int64)
-    o = _lib.AdamwOptions(p0 == torch.bfloat16, g0 == torch.bfloat16, step, lr, betas[0], betas[1], eps, weight_decay)
-    with _on_device(m):
-        check(lib.soup_adamw_multi(table.ctypes.data, n, byref(o), m.data_ptr(), v.data_ptr(), _ptr(m_scale), _ptr(v_scale),
-                                   _ptr(hp), _stream_ptr()))
+    _calls.adamw_multi(params, grads, m, v, m_scale, v_scale, hp, lr, step, betas[0], betas[1], eps, weight_decay)
 
 
 def adamw_state_values(m: torch.Tensor, v: torch.Tensor, m_scale: torch.Tensor, v_scale: torch.Tensor):
     """(m, v) in bf16: the values that 8-bit states stand for, in the states' layout."""
-    _need(m.dtype == torch.int8 and v.dtype == torch.uint8 and m.is_cuda and m.numel() == v.numel() == 256 * m_scale.numel()
-          and v_scale.numel() == m_scale.numel() and v.device == m.device and m_scale.device == v_scale.device == m.device
-          and m_scale.dtype == v_scale.dtype == torch.float32
-          and all(t.is_contiguous() for t in (m, v, m_scale, v_scale)), "adamw: 8-bit states and their scales")
-    with _on_device(m):
-        mo, vo = torch.empty_like(m, dtype=torch.bfloat16), torch.empty_like(v, dtype=torch.bfloat16)
-        check(lib.soup_adamw_state_values(m.data_ptr(), v.data_ptr(), m_scale.data_ptr(), v_scale.data_ptr(), m.numel(),
-                                          mo.data_ptr(), vo.data_ptr(), _stream_ptr()))
-    return mo, vo
+    return _calls.adamw_state_values(m, v, m_scale, v_scale)
 
 
 def rope_config(rotary_dim: int, theta: float = 10000.0, interleaved: bool = False, scaling: str = "none",
@@ -528,6 +449,11 @@ def rope_config(rotary_dim: int, theta: float = 10000.0, interleaved: bool = Fal
     _need(scaling in _lib.ROPE_SCALING, f"rope: scaling is one of {sorted(_lib.ROPE_SCALING)}")
     return _lib.RopeConfig(int(rotary_dim), 1 if interleaved else 0, _lib.ROPE_SCALING[scaling], int(original_len),
                            float(theta), float(factor), float(low_freq_factor), float(high_freq_factor))
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_bytes(*config) -> bytes:
+    return bytes(rope_config(*config))
 
 
 def rope_frequencies(cfg: _lib.RopeConfig):
@@ -543,25 +469,6 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, theta
     """Rotary positions of q [T, heads, d] and k [T, heads_k, d] (or None), bf16 or fp32, tokens any
     stride apart (views of a packed q|k|v are fine).  positions: int32 [T].  Returns (q, k), new tensors
     unless inplace.  inverse: the rotation back, which is the gradient."""
-    T, d = q.shape[0], q.shape[-1]
-    cfg = rope_config(d if rotary_dim is None else rotary_dim, theta, interleaved, scaling, factor, original_len,
+    cfg = _rope_bytes(q.shape[-1] if rotary_dim is None else rotary_dim, theta, interleaved, scaling, factor, original_len,
                       low_freq_factor, high_freq_factor)
-    _need(q.is_cuda and q.dtype in (torch.bfloat16, torch.float32) and positions.dtype == torch.int32 and
-          positions.shape == (T,) and positions.device == q.device and positions.is_contiguous(),
-          "rope: bf16 or fp32 q on a GPU and contiguous int32 positions [T] beside it")
-    for x in (q, k):
-        _need(x is None or (x.dim() == 3 and x.shape[0] == T and x.shape[2] == d and x.dtype == q.dtype and
-                            x.device == q.device and (x.stride(2) == 1 or d == 1) and
-                            (x.stride(1) == d or x.shape[1] == 1)),
-              "rope: [T, heads, d] with contiguous heads, k like q")
-    with _on_device(q):
-        if inplace:
-            qo, ko = q, k
-        else:
-            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        hk = 0 if k is None else k.shape[1]
-        check(lib.soup_rope(byref(cfg), q.data_ptr(), q.stride(0), qo.data_ptr(), qo.stride(0), q.shape[1], _ptr(k),
-                            0 if k is None else k.stride(0), _ptr(ko), 0 if k is None else ko.stride(0), hk, d, T,
-                            positions.data_ptr(), 1 if q.dtype == torch.float32 else 0, 1 if inverse else 0, _stream_ptr()))
-    return qo, ko
+    return _calls.rope(cfg, q, k, positions, inverse, inplace)
