@@ -62,6 +62,13 @@ typedef enum {
   SOUP_LOSS_SIMPO = 4  /* reference-free */
 } soup_loss;
 
+/* Rotary positions; what the fields mean stands at soup_rope. */
+enum { SOUP_ROPE_NONE = 0, SOUP_ROPE_LINEAR, SOUP_ROPE_NTK, SOUP_ROPE_BY_PARTS, SOUP_ROPE_YARN };
+typedef struct soup_rope_config {
+  int rotary_dim, interleaved, scaling, original_len;
+  double theta, factor, low_freq_factor, high_freq_factor;
+} soup_rope_config;
+
 /* Model shape and run options.  Decoder layer = pre-norm Llama block (RMSNorm, GQA attention
  * with rotate-half RoPE, SwiGLU MLP), LoRA on all seven projections with scale alpha/r. */
 typedef struct soup_model_config {
@@ -158,6 +165,19 @@ typedef struct soup_batch {
  * when an allocation (or the caller's allocator) fails; nothing is leaked on failure.
  * soup_model_destroy frees everything the model holds (NULL: SOUP_ERR_INVALID_ARG). */
 soup_status soup_model_create(const soup_model_config* cfg, const soup_allocator* alloc, soup_model** out);
+/* soup_model_create with options (NULL or all zero: the same model).
+ *   loss_in_pieces: soup_step's loss and its gradient by soup_linear_ce's kernels.  The fp32 logits and bf16
+ *       gradients of max_tokens x vocab (6 bytes each pair) are then not allocated, which is what limits a long
+ *       context in little memory, and rows that are no target (masked, prefix) cost nothing in the head.  The
+ *       same loss up to rounding.  SOUP_ERR_UNSUPPORTED beyond soup_linear_ce's sizes.
+ *   rope: the layers' rotary positions in place of cfg.rope_theta, for contexts beyond the base model's own.
+ *       Read during the call.  SOUP_ERR_UNSUPPORTED unless rotary_dim = head_dim and interleaved = 0. */
+typedef struct soup_model_options {
+  int loss_in_pieces;
+  const soup_rope_config* rope;
+} soup_model_options;
+soup_status soup_model_create_with(const soup_model_config* cfg, const soup_model_options* options,
+                                   const soup_allocator* alloc, soup_model** out);
 soup_status soup_model_destroy(soup_model* model);
 
 /* Bytes of one layer's NF4 blob (7 projections: codes, q8 absmax, fp32 group scales, fp32
@@ -208,6 +228,13 @@ soup_status soup_lora_numel(const soup_model_config* cfg, size_t* numel);
 soup_status soup_lora_offset(const soup_model_config* cfg, int layer, int proj, int which_b, size_t* offset,
                              int* rows, int* cols);
 soup_status soup_model_set_lora(soup_model* model, float* params, float* grads, float* adam_m, float* adam_v);
+/* soup_model_set_lora with 8-bit optimizer states (soup_adamw_multi's): m int8 and v uint8 of
+ * soup_lora_state_numel elements, 32-byte aligned, each layer's slice from a whole block on, and an fp32
+ * scale for each SOUP_ADAMW_BLOCK of them; all zero at the start.  soup_step and soup_optimizer_step update
+ * them.  2 bytes an adapter parameter in place of 8. */
+soup_status soup_lora_state_numel(const soup_model_config* cfg, size_t* numel);
+soup_status soup_model_set_lora_adam8(soup_model* model, float* params, float* grads, void* adam_m, void* adam_v,
+                                      float* m_scale, float* v_scale);
 /* Sets the adapters of one projection: copies A [r, in] and B [out, r] (fp32, row-major, host
  * or device memory) into the parameter buffer given to soup_model_set_lora, at the place
  * soup_lora_offset names, and refreshes their bf16 copy; enqueued on `stream`.  The adapters
@@ -364,7 +391,8 @@ soup_status soup_linear_ce_bwd(const void* w, long long ldw, int T, int hidden, 
  * a zero state is all zeros either way.  Arithmetic is fp32 whatever the types; p (fp32 or bf16) is
  * rounded once.  p_bf16_copy (may be NULL) receives p' rounded to bf16.  hp (device float[3], may be NULL):
  * lr, 1/(1-b1^step), 1/(1-b2^step) read on the device in place of lr and step, for captured graphs.
- * tensors is a host array, read during the call.  A tensor of n = 0 is allowed.  SOUP_ERR_INVALID_ARG
+ * tensors is a host array, read during the call; tensors do not overlap.  A tensor of n = 0 is allowed.
+ * |g| is below 10^17: v' times 2^24 c has to fit in fp32.  SOUP_ERR_INVALID_ARG
  * for null pointers, n < 0, step < 1 (without hp), v_scale without m_scale or the reverse, a
  * state address not 32-byte aligned, or tensors not aligned to their own type. */
 #define SOUP_ADAMW_BLOCK 256
@@ -398,14 +426,9 @@ soup_status soup_adamw_state_values(const void* m, const void* v, const float* m
  *   YARN (Peng et al. 2023): as BY_PARTS, and cos, sin times 1 + 0.1 ln factor
  * inverse != 0 applies the transpose, which is the gradient.  dtype 0: bf16, 1: fp32; angles are formed in
  * 64 bits and the result rounded once.  positions: device int32 [T].  The library's own decoder
- * layers take the same configuration (soup_model_config.rope).  SOUP_ERR_INVALID_ARG for a bad
+ * layers take the same configuration (soup_model_options.rope).  SOUP_ERR_INVALID_ARG for a bad
  * configuration, null pointers, strides below heads x head_dim, or addresses not aligned to the type;
  * SOUP_ERR_UNSUPPORTED for rotary_dim odd, above head_dim or above 256.  T = 0 does nothing. */
-enum { SOUP_ROPE_NONE = 0, SOUP_ROPE_LINEAR, SOUP_ROPE_NTK, SOUP_ROPE_BY_PARTS, SOUP_ROPE_YARN };
-typedef struct soup_rope_config {
-  int rotary_dim, interleaved, scaling, original_len;
-  double theta, factor, low_freq_factor, high_freq_factor;
-} soup_rope_config;
 /* Host only: the rotary_dim / 2 frequencies (radians a position) and the factor on cos and sin. */
 soup_status soup_rope_frequencies(const soup_rope_config* cfg, double* freq, double* factor_on_cos_sin);
 soup_status soup_rope(const soup_rope_config* cfg, const void* q, long long ldq, void* q_out, long long ldq_out, int heads_q,

@@ -74,6 +74,10 @@ class AdamwTensor(Structure):
     _fields_ = [("p", c_void_p), ("g", c_void_p), ("p_bf16_copy", c_void_p), ("n", c_longlong)]
 
 
+class ModelOptions(Structure):
+    _fields_ = [("loss_in_pieces", c_int), ("rope", c_void_p)]
+
+
 class RopeConfig(Structure):
     _fields_ = [("rotary_dim", c_int), ("interleaved", c_int), ("scaling", c_int), ("original_len", c_int),
                 ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("low_freq_factor", ctypes.c_double),
@@ -89,6 +93,7 @@ class Batch(Structure):
 
 # name -> (restype, argtypes); every function returns soup_status unless stated
 SIGNATURES = {
+    "soup_model_create_with": [POINTER(ModelConfig), POINTER(ModelOptions), c_void_p, POINTER(c_void_p)],
     "soup_model_create": [POINTER(ModelConfig), POINTER(Allocator), POINTER(c_void_p)],
     "soup_model_destroy": [c_void_p],
     "soup_layer_blob_bytes": [POINTER(ModelConfig), POINTER(c_size_t)],
@@ -100,6 +105,8 @@ SIGNATURES = {
     "soup_model_set_head": [c_void_p, c_void_p, c_void_p, c_void_p],
     "soup_lora_numel": [POINTER(ModelConfig), POINTER(c_size_t)],
     "soup_lora_offset": [POINTER(ModelConfig), c_int, c_int, c_int, POINTER(c_size_t), POINTER(c_int), POINTER(c_int)],
+    "soup_lora_state_numel": [POINTER(ModelConfig), POINTER(c_size_t)],
+    "soup_model_set_lora_adam8": [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p],
     "soup_model_set_lora": [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p],
     "soup_set_lora_enabled": [c_void_p, c_int],
     "soup_model_set_lora_proj": [c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p],

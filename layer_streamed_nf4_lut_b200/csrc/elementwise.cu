@@ -395,6 +395,23 @@ __global__ void pair_pack_kernel(const int32_t* __restrict__ ids, int P, int S, 
   tgt2[x_all] = t2;
 }
 
+// The targets that count, -1 elsewhere.  Plain rows t = (b, s): the next token, from position `first` on
+// and where the mask is set.  Packed rows of a pair block: the pack's first target, from the last prefix
+// row (first = prefix length) on.
+__global__ void ce_targets_kernel(const int32_t* __restrict__ src, const uint8_t* __restrict__ mask, int T, int S, int first,
+                                  int packed, int32_t* __restrict__ out) {
+  const int t = blockIdx.x * blockDim.x + threadIdx.x;
+  if (t >= T) return;
+  const int s = t % S;
+  int y = -1;
+  if (packed) {
+    if (s >= first - 1) y = src[t];
+  } else if (s + 1 < S && s + 1 >= first && (mask == nullptr || mask[t + 1] != 0)) {
+    y = src[t + 1];
+  }
+  out[t] = y;
+}
+
 // Row LSE and the logits at tgt1 / tgt2 (0 where there is no target).
 __global__ void ce_rows_t_kernel(const float* __restrict__ logits, int V, const int32_t* __restrict__ tgt1,
                                  const int32_t* __restrict__ tgt2, float* __restrict__ lse, float* __restrict__ rt1,
@@ -745,6 +762,14 @@ cudaError_t pair_pack_launch(const int32_t* ids, int P, int S, int pl, int V, in
   const long long n = static_cast<long long>(P) * (2 * S - pl);
   if (n <= 0) return cudaSuccess;
   pair_pack_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, st>>>(ids, P, S, pl, V, pids, tgt1, tgt2, err);
+  ++g_kernel_launches;
+  return cudaGetLastError();
+}
+
+cudaError_t ce_targets_launch(const int32_t* src, const uint8_t* mask, int T, int S, int first, bool packed, int32_t* out,
+                              cudaStream_t st) {
+  if (T <= 0) return cudaSuccess;
+  ce_targets_kernel<<<static_cast<unsigned>((T + 255) / 256), 256, 0, st>>>(src, mask, T, S, first, packed ? 1 : 0, out);
   ++g_kernel_launches;
   return cudaGetLastError();
 }

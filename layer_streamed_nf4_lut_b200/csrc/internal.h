@@ -280,6 +280,9 @@ cudaError_t f32_to_bf16_launch(const float* x, uint16_t* y, long long n, cudaStr
 cudaError_t fill_zero_launch(void* p, size_t bytes, cudaStream_t st);
 
 // ----------------------------------------------------------------- loss over the vocabulary in pieces
+// elementwise.cu: the targets that count of a step's rows
+cudaError_t ce_targets_launch(const int32_t* src, const uint8_t* mask, int T, int S, int first, bool packed, int32_t* out,
+                              cudaStream_t st);
 // linear_ce.cu.  ws: linear_ce_workspace(T, H, V, grad) bytes, 256-byte aligned; a gradient call reads
 // what the forward call with grad left there.
 size_t linear_ce_workspace(int T, int H, int V, bool grad);

@@ -79,6 +79,7 @@ const LUT16& codebook() {
 
 // ------------------------------------------------------------------ shapes and blob layout
 constexpr size_t ALIGN = 256;
+bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 size_t align_up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
 
 struct ProjShape {
@@ -237,6 +238,10 @@ struct soup_model {
   const uint16_t* lm_head = nullptr;
   // LoRA storage
   float *lora_p = nullptr, *lora_g = nullptr, *lora_m = nullptr, *lora_v = nullptr;
+  // 8-bit optimizer states (soup_model_set_lora_adam8), each layer's slice from a whole block on; set
+  // in place of lora_m and lora_v
+  uint8_t *lora_m8 = nullptr, *lora_v8 = nullptr;
+  float *lora_m_scale = nullptr, *lora_v_scale = nullptr;
   uint16_t* lora_bf16 = nullptr;  // bf16 copy of the parameters: the GEMM operands
   size_t lora_n = 0;
   int lora_enabled = 1;
@@ -265,6 +270,10 @@ struct soup_model {
   int pack_pl = 0, pack_rl = 0;  // non-zero while a packed step runs
   int32_t *pids = nullptr, *tgt1 = nullptr, *tgt2 = nullptr;
   float *rowtgt2 = nullptr, *roww2 = nullptr, *seqw = nullptr;
+  // loss in pieces of the vocabulary (soup_model_options): its workspace, and the targets that count
+  uint8_t* ce_ws = nullptr;
+  size_t ce_ws_bytes = 0;
+  int32_t* ce_tgt = nullptr;
   // scalars: [0] loss (f32), [1] device error word (int)
   int* scal = nullptr;
   float* quant_scratch = nullptr;  // absmax scratch for the quantiser
@@ -953,10 +962,28 @@ constexpr float ADAM_B1 = 0.9f, ADAM_B2 = 0.999f, ADAM_EPS = 1e-8f, ADAM_WD = 0.
 
 bool adam_after(const soup_model* m, int i) { return m->adam_in_bwd && m->lora_p && i + 1 < m->cfg.n_layers; }
 
+// Blocks of 8-bit states of a layer's slice.
+size_t lora_layer_blocks(const soup_model_config& c) { return (lora_layer_numel(c) + ADAMW_BLOCK - 1) / ADAMW_BLOCK; }
+
+// AdamW on the slices of layers [l0, l1) with 8-bit states; hp as in soup_adamw_multi.
+cudaError_t adamw8_layers(soup_model* m, int l0, int l1, float lr, const float* hp, cudaStream_t st) {
+  const size_t n = lora_layer_numel(m->cfg), blocks = lora_layer_blocks(m->cfg), b0 = blocks * static_cast<size_t>(l0);
+  std::vector<soup_adamw_tensor> t;
+  for (int l = l0; l < l1; ++l) {
+    const size_t off = lora_off(m->cfg, l, 0, 0);
+    t.push_back({m->lora_p + off, m->lora_g + off, m->lora_bf16 + off, static_cast<long long>(n)});
+  }
+  const soup_adamw_options o{0, 0, m->adam_t, lr, ADAM_B1, ADAM_B2, ADAM_EPS, ADAM_WD};
+  return adamw_multi_launch(t.data(), static_cast<int>(t.size()), o, m->lora_m8 + b0 * ADAMW_BLOCK,
+                            m->lora_v8 + b0 * ADAMW_BLOCK, m->lora_m_scale + b0, m->lora_v_scale + b0, hp, st);
+}
+
 // AdamW on layer l's LoRA slice with the step's hyper-parameters from device memory.
 soup_status adamw_layer(soup_model* m, int l, cudaStream_t st) {
   const size_t off = lora_off(m->cfg, l, 0, 0), n = lora_layer_numel(m->cfg);
   const float* hp = reinterpret_cast<const float*>(m->scal + ADAM_HP_WORD);
+  if (m->lora_m8)
+    return launch(m, st, CAT_ADAMW, 0, 18.0 * static_cast<double>(n), "adamw", [&] { return adamw8_layers(m, l, l + 1, 0.f, hp, st); });
   return launch(m, st, CAT_ADAMW, 0, 28.0 * static_cast<double>(n), "adamw", [&] {
     return adamw_hp_launch(m->lora_p + off, m->lora_g + off, m->lora_m + off, m->lora_v + off,
                            m->lora_bf16 ? m->lora_bf16 + off : nullptr, static_cast<long long>(n), ADAM_B1, ADAM_B2,
@@ -1107,12 +1134,27 @@ soup_status layer_backward_body(soup_model* m, int i, const LayerView& L, const 
 
 // ------------------------------------------------------------------ head
 // logits = RMSNorm(x) W_lm^T (fp32), per-row LSE and target logit.
-soup_status head_forward(soup_model* m, const uint16_t* x, int B, int S, cudaStream_t st) {
+// first, mask: the targets that count (for the loss in pieces; the others' rows are left out of it);
+// grad: what the backward pass needs is kept.
+soup_status head_forward(soup_model* m, const uint16_t* x, int B, int S, int first, const uint8_t* mask, bool grad,
+                         cudaStream_t st) {
   const NvtxRange trace("head fwd");
   const soup_model_config& c = m->cfg;
   const int T = B * S, h = c.hidden, V = c.vocab;
   SOUP_TRY(launch(m, st, CAT_RMSNORM, 0, 4.0 * T * h + 4.0 * T, "final norm",
                   [&] { return rmsnorm_fwd_launch(x, m->final_gamma, T, h, c.rms_eps, m->hf, m->rstdf, st); }));
+  if (m->ce_ws) {
+    const bool packed = m->pack_pl > 0;
+    SOUP_TRY(check_launch(m, ce_targets_launch(packed ? m->tgt1 : m->ids_dev, packed ? nullptr : mask, T, S,
+                                               packed ? m->pack_pl : first, packed, m->ce_tgt, st),
+                          "loss targets"));
+    const double flops = (grad ? 4.0 : 2.0) * T * static_cast<double>(V) * h;
+    SOUP_TRY(launch(m, st, CAT_CE, flops, 2.0 * V * h, "loss in pieces", [&] {
+      return linear_ce_fwd_launch(m->hf, h, m->lm_head, h, T, h, V, m->ce_tgt, packed ? m->tgt2 : nullptr, grad, nullptr,
+                                  m->rowtgt, packed ? m->rowtgt2 : nullptr, m->ce_ws, m->scal + 1, st);
+    }));
+    return SOUP_OK;
+  }
   GemmParams p = gemm_base(m, T, V, m->logits, V, 1, 1.f);
   add_seg(p, h, opnd(OP_BF16_K, m->hf, h), opnd(OP_BF16_K, m->lm_head, h));
   SOUP_TRY(run_gemm(m, p, st, "lm_head"));
@@ -1132,6 +1174,14 @@ soup_status head_backward(soup_model* m, const uint16_t* x, int B, int S, uint16
   const NvtxRange trace("head bwd");
   const soup_model_config& c = m->cfg;
   const int T = B * S, h = c.hidden, V = c.vocab;
+  if (m->ce_ws) {
+    SOUP_TRY(launch(m, st, CAT_CE, 0, 6.0 * T * h, "loss gradient", [&] {
+      return linear_ce_bwd_launch(m->lm_head, h, T, h, V, m->roww, m->pack_pl > 0 ? m->roww2 : nullptr, m->dh, h, m->ce_ws, st);
+    }));
+    SOUP_TRY(launch(m, st, CAT_RMSNORM, 0, 6.0 * T * h + 4.0 * T, "final norm bwd",
+                    [&] { return rmsnorm_bwd_launch(m->dh, x, m->rstdf, m->final_gamma, nullptr, T, h, dx, st); }));
+    return SOUP_OK;
+  }
   SOUP_TRY(launch(m, st, CAT_CE, 0, 6.0 * T * V, "ce grad", [&] {
     return m->pack_pl > 0
                ? ce_grad_t_launch(m->logits, m->rowlse, m->tgt1, m->roww, m->tgt2, m->roww2, T, V, m->dlogits, st)
@@ -1387,6 +1437,8 @@ soup_status do_step_body(soup_model* m, soup_loss kind, const soup_batch* bt, fl
   SOUP_CK(cudaMemsetAsync(m->lora_g, 0, m->lora_n * sizeof(float), st));
   const int saved_enabled = m->lora_enabled;
   uint16_t* xL = nullptr;
+  const int first = kind == SOUP_LOSS_SFT ? 1 : std::max(bt->prefix_len, 1);  // first position that counts as a target
+  if (kind != SOUP_LOSS_SFT) mask = nullptr;
   if (needs_ref && bt->dpo_shared_load) {
     SOUP_TRY(streamer_warm(m, 0, 2));
     SOUP_TRY(launch(m, st, CAT_EMBED, 0, 4.0 * Tx * c.hidden, "embed", [&] {
@@ -1397,12 +1449,12 @@ soup_status do_step_body(soup_model* m, soup_loss kind, const soup_batch* bt, fl
     }));
     uint16_t* xR = nullptr;
     SOUP_TRY(stream_forward_pass_shared(m, Bx, Sx, st, &xR, &xL));
-    SOUP_TRY(head_forward(m, xR, Bx, Sx, st));
+    SOUP_TRY(head_forward(m, xR, Bx, Sx, first, mask, false, st));
     SOUP_TRY(check_launch(m,
                           share ? pair_logp_launch(m->rowlse, m->rowtgt, m->rowtgt2, Bx, pl, rl, m->ref, st)
                                 : seq_logp_launch(m->rowlse, m->rowtgt, B, S, bt->prefix_len, m->ref, st),
                           "ref logp"));
-    SOUP_TRY(head_forward(m, xL, Bx, Sx, st));
+    SOUP_TRY(head_forward(m, xL, Bx, Sx, first, mask, true, st));
   } else {
   if (needs_ref) {
     // reference: same streamed base, LoRA off
@@ -1416,7 +1468,7 @@ soup_status do_step_body(soup_model* m, soup_loss kind, const soup_batch* bt, fl
       m->lora_enabled = saved_enabled;
       return s1;
     }
-    SOUP_TRY(head_forward(m, xL, Bx, Sx, st));
+    SOUP_TRY(head_forward(m, xL, Bx, Sx, first, mask, false, st));
     SOUP_TRY(check_launch(m,
                           share ? pair_logp_launch(m->rowlse, m->rowtgt, m->rowtgt2, Bx, pl, rl, m->ref, st)
                                 : seq_logp_launch(m->rowlse, m->rowtgt, B, S, bt->prefix_len, m->ref, st),
@@ -1430,7 +1482,7 @@ soup_status do_step_body(soup_model* m, soup_loss kind, const soup_batch* bt, fl
   soup_status s2 = stream_forward_pass(m, Bx, Sx, st, &xL);
   m->lora_enabled = saved_enabled;
   if (s2 != SOUP_OK) return s2;
-  SOUP_TRY(head_forward(m, xL, Bx, Sx, st));
+  SOUP_TRY(head_forward(m, xL, Bx, Sx, first, mask, true, st));
   }
   float* loss_dev = reinterpret_cast<float*>(m->scal);
   if (share) {
@@ -1526,11 +1578,26 @@ soup_status destroy_model(soup_model* m) {
   return SOUP_OK;
 }
 
-soup_status create_model(const soup_model_config* cfg, const soup_allocator* alloc, soup_model** out) {
+soup_status linear_ce_sizes(int T, int hidden, int vocab) {
+  if (T < 0 || hidden < 1 || vocab < 1) return SOUP_ERR_INVALID_ARG;
+  return (hidden % 8 || T >= (1 << 24) || hidden > (1 << 16) || vocab > (1 << 22)) ? SOUP_ERR_UNSUPPORTED : SOUP_OK;
+}
+
+// The layers rotate whole heads, halves against each other.
+soup_status validate_rope(const soup_model_config& c, const soup_rope_config& r) {
+  std::string why;
+  if (!rope_config_ok(r, why)) return SOUP_ERR_INVALID_ARG;
+  return r.rotary_dim == c.head_dim && !r.interleaved ? SOUP_OK : SOUP_ERR_UNSUPPORTED;
+}
+
+soup_status create_model(const soup_model_config* cfg, const soup_model_options* opt, const soup_allocator* alloc,
+                         soup_model** out) {
   soup_model* m = new soup_model();
   m->cfg = *cfg;
   std::string why;
   soup_status vs = validate_cfg(*cfg, why);
+  if (vs == SOUP_OK && opt && opt->rope) vs = validate_rope(*cfg, *opt->rope);
+  if (vs == SOUP_OK && opt && opt->loss_in_pieces) vs = linear_ce_sizes(cfg->max_tokens, cfg->hidden, cfg->vocab);
   if (vs != SOUP_OK) {
     delete m;
     return vs;
@@ -1623,22 +1690,39 @@ soup_status create_model(const soup_model_config* cfg, const soup_allocator* all
       alloc_into(m, m->dgu, T * 2 * I) || alloc_into(m, m->dm, T * I) || alloc_into(m, m->da, T * qd) ||
       alloc_into(m, m->dn, T * h) || alloc_into(m, m->dx1, T * h) || alloc_into(m, m->vqkv, T * 3 * r) ||
       alloc_into(m, m->vo, T * r) || alloc_into(m, m->vgu, T * 2 * r) || alloc_into(m, m->vd, T * r) ||
-      alloc_into(m, m->hf, T * h) || alloc_into(m, m->dh, T * h) || alloc_into(m, m->dlogits, T * V) ||
-      alloc_into(m, m->delta, T * c.n_heads) || alloc_into(m, m->logits, T * V) || alloc_into(m, m->rowlse, T) ||
+      alloc_into(m, m->hf, T * h) || alloc_into(m, m->dh, T * h) ||
+      alloc_into(m, m->delta, T * c.n_heads) || alloc_into(m, m->rowlse, T) ||
       alloc_into(m, m->rowtgt, T) || alloc_into(m, m->roww, T) || alloc_into(m, m->rstdf, T) ||
       alloc_into(m, m->pi, T) || alloc_into(m, m->ref, T) || alloc_into(m, m->ids_dev, T) ||
       alloc_into(m, m->mask_dev, T) || alloc_into(m, m->labels_dev, T) || alloc_into(m, m->pids, T) ||
       alloc_into(m, m->tgt1, T) || alloc_into(m, m->tgt2, T) || alloc_into(m, m->rowtgt2, T) ||
       alloc_into(m, m->roww2, T) || alloc_into(m, m->seqw, 256) || alloc_into(m, m->scal, 64))
     return fail(SOUP_ERR_OOM);
+  if (opt && opt->loss_in_pieces) {
+    // a step has any number of rows up to max_tokens: the largest need of all
+    for (size_t t = std::min<size_t>(256, T);; t = std::min(t + 256, T)) {
+      m->ce_ws_bytes = std::max(m->ce_ws_bytes, linear_ce_workspace(static_cast<int>(t), c.hidden, c.vocab, true));
+      if (t == T) break;
+    }
+    if (alloc_into(m, m->ce_ws, m->ce_ws_bytes) || alloc_into(m, m->ce_tgt, T)) return fail(SOUP_ERR_OOM);
+    // this loss hands on log-probs, which take the place of the targets' logits beside a row LSE of zero
+    if (cudaMemset(m->rowlse, 0, T * sizeof(float)) != cudaSuccess) return fail(SOUP_ERR_CUDA);
+  } else if (alloc_into(m, m->dlogits, T * V) || alloc_into(m, m->logits, T * V)) {
+    return fail(SOUP_ERR_OOM);
+  }
   {  // RoPE tables: angle = pos * theta^(-2i/d), computed in float64, stored as float32
     const int half = c.head_dim / 2;
+    // a given configuration's frequencies, and its factor on cos and sin
+    std::vector<double> freq(static_cast<size_t>(half));
+    double grow = 1.0;
+    if (opt && opt->rope) rope_frequencies(*opt->rope, freq.data(), &grow);
     std::vector<float> hc(static_cast<size_t>(T) * half), hs(hc.size());
     for (size_t pos = 0; pos < T; ++pos)
       for (int i = 0; i < half; ++i) {
-        const double ang = static_cast<double>(pos) * std::pow(static_cast<double>(c.rope_theta), -2.0 * i / c.head_dim);
-        hc[pos * half + i] = static_cast<float>(std::cos(ang));
-        hs[pos * half + i] = static_cast<float>(std::sin(ang));
+        const double ang = static_cast<double>(pos) * (opt && opt->rope ? freq[static_cast<size_t>(i)]
+                                                                        : std::pow(static_cast<double>(c.rope_theta), -2.0 * i / c.head_dim));
+        hc[pos * half + i] = static_cast<float>(grow * std::cos(ang));
+        hs[pos * half + i] = static_cast<float>(grow * std::sin(ang));
       }
     if (alloc_into(m, m->rope_cos, hc.size()) || alloc_into(m, m->rope_sin, hs.size())) return fail(SOUP_ERR_OOM);
     if (cudaMemcpy(m->rope_cos, hc.data(), hc.size() * 4, cudaMemcpyHostToDevice) != cudaSuccess ||
@@ -1802,10 +1886,15 @@ soup_status soup_lora_offset(const soup_model_config* cfg, int layer, int proj, 
   return SOUP_OK;
 }
 
-soup_status soup_model_create(const soup_model_config* cfg, const soup_allocator* alloc, soup_model** out) {
+soup_status soup_model_create_with(const soup_model_config* cfg, const soup_model_options* options,
+                                   const soup_allocator* alloc, soup_model** out) {
   soup_model* m = nullptr;
   if (!cfg || !out) return SOUP_ERR_INVALID_ARG;
-  SOUP_GUARD(return create_model(cfg, alloc, out);)
+  SOUP_GUARD(return create_model(cfg, options, alloc, out);)
+}
+
+soup_status soup_model_create(const soup_model_config* cfg, const soup_allocator* alloc, soup_model** out) {
+  return soup_model_create_with(cfg, nullptr, alloc, out);
 }
 
 soup_status soup_model_destroy(soup_model* m) {
@@ -1910,18 +1999,12 @@ soup_status soup_model_set_head(soup_model* m, const void* embed, const void* fi
   return SOUP_OK;
 }
 
-soup_status soup_model_set_lora(soup_model* m, float* params, float* grads, float* adam_m, float* adam_v) {
-  if (!m || !params || !grads || !adam_m || !adam_v) return SOUP_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(params) | reinterpret_cast<uintptr_t>(grads) | reinterpret_cast<uintptr_t>(adam_m) |
-       reinterpret_cast<uintptr_t>(adam_v)) & 15u) {
-    m->err = "LoRA buffers must be 16-byte aligned";
-    return SOUP_ERR_INVALID_ARG;
-  }
+static soup_status set_lora(soup_model* m, float* params, float* grads) {
   clear_graphs(m);
   m->lora_p = params;
   m->lora_g = grads;
-  m->lora_m = adam_m;
-  m->lora_v = adam_v;
+  m->lora_m = m->lora_v = m->lora_m_scale = m->lora_v_scale = nullptr;
+  m->lora_m8 = m->lora_v8 = nullptr;
   m->adam_t = 0;
   for (auto& a : m->saved) a.valid = 0;
   SOUP_GUARD({
@@ -1930,6 +2013,43 @@ soup_status soup_model_set_lora(soup_model* m, float* params, float* grads, floa
     SOUP_CK(cudaDeviceSynchronize());
     return SOUP_OK;
   })
+}
+
+soup_status soup_lora_state_numel(const soup_model_config* cfg, size_t* numel) {
+  if (!cfg || !numel) return SOUP_ERR_INVALID_ARG;
+  std::string why;
+  SOUP_TRY(validate_cfg(*cfg, why));
+  *numel = lora_layer_blocks(*cfg) * ADAMW_BLOCK * static_cast<size_t>(cfg->n_layers);
+  return SOUP_OK;
+}
+
+soup_status soup_model_set_lora_adam8(soup_model* m, float* params, float* grads, void* adam_m, void* adam_v, float* m_scale,
+                                      float* v_scale) {
+  if (!m || !params || !grads || !adam_m || !adam_v || !m_scale || !v_scale) return SOUP_ERR_INVALID_ARG;
+  if (misaligned(params, 16) || misaligned(grads, 16) || misaligned(adam_m, 32) || misaligned(adam_v, 32) ||
+      misaligned(m_scale, 4) || misaligned(v_scale, 4)) {
+    m->err = "LoRA buffers must be 16-byte aligned, their 8-bit states 32-byte";
+    return SOUP_ERR_INVALID_ARG;
+  }
+  SOUP_TRY(set_lora(m, params, grads));
+  m->lora_m8 = static_cast<uint8_t*>(adam_m);
+  m->lora_v8 = static_cast<uint8_t*>(adam_v);
+  m->lora_m_scale = m_scale;
+  m->lora_v_scale = v_scale;
+  return SOUP_OK;
+}
+
+soup_status soup_model_set_lora(soup_model* m, float* params, float* grads, float* adam_m, float* adam_v) {
+  if (!m || !params || !grads || !adam_m || !adam_v) return SOUP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(params) | reinterpret_cast<uintptr_t>(grads) | reinterpret_cast<uintptr_t>(adam_m) |
+       reinterpret_cast<uintptr_t>(adam_v)) & 15u) {
+    m->err = "LoRA buffers must be 16-byte aligned";
+    return SOUP_ERR_INVALID_ARG;
+  }
+  SOUP_TRY(set_lora(m, params, grads));
+  m->lora_m = adam_m;
+  m->lora_v = adam_v;
+  return SOUP_OK;
 }
 
 soup_status soup_model_set_lora_proj(soup_model* m, int layer, int proj, const float* A, const float* B,
@@ -2062,6 +2182,11 @@ soup_status soup_optimizer_step(soup_model* m, float lr, void* stream) {
   SOUP_GUARD({
     m->adam_t += 1;
     const long long l0 = g_kernel_launches.load();
+    if (m->lora_m8) {
+      soup_status s8 = check_launch(m, adamw8_layers(m, 0, m->cfg.n_layers, lr, nullptr, static_cast<cudaStream_t>(stream)), "adamw");
+      m->stats.kernel_launches += g_kernel_launches.load() - l0;
+      return s8;
+    }
     soup_status s = check_launch(m, adamw_launch(m->lora_p, m->lora_g, m->lora_m, m->lora_v, m->lora_bf16,
                                                  static_cast<long long>(m->lora_n), lr, ADAM_B1, ADAM_B2, ADAM_EPS,
                                                  ADAM_WD, m->adam_t, static_cast<cudaStream_t>(stream)),
@@ -2169,14 +2294,9 @@ soup_status soup_nf4_matmul(const void* x, int M, int N, int K, const uint8_t* c
 
 // ---- loss in pieces of the vocabulary, AdamW over many tensors, rotary positions
 namespace {
-bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 soup_status of_launch(cudaError_t e) {
   if (e == cudaSuccess) return SOUP_OK;
   return e == cudaErrorInvalidValue ? SOUP_ERR_INVALID_ARG : SOUP_ERR_CUDA;
-}
-soup_status linear_ce_sizes(int T, int hidden, int vocab) {
-  if (T < 0 || hidden < 1 || vocab < 1) return SOUP_ERR_INVALID_ARG;
-  return (hidden % 8 || T >= (1 << 24) || hidden > (1 << 16) || vocab > (1 << 22)) ? SOUP_ERR_UNSUPPORTED : SOUP_OK;
 }
 }  // namespace
 

@@ -95,16 +95,19 @@ class _TorchAllocator:
 
 class SoupModel:
     def __init__(self, cfg: dict, mode: str = "streamed", n_layer_buffers: int = 2, max_tokens: int | None = None,
-                 device: int = 0, torch_alloc: bool = True, source: str = "ram", stack_path: str | None = None):
+                 device: int = 0, torch_alloc: bool = True, source: str = "ram", stack_path: str | None = None,
+                 loss_in_pieces: bool = False, rope: _lib.RopeConfig | None = None):
         """source: "ram" (page-locked host stack), "file" (stack file at stack_path, streamed
-        through page-locked staging) or "auto" (RAM if it fits, else the file)."""
+        through page-locked staging) or "auto" (RAM if it fits, else the file).  loss_in_pieces: the
+        step's loss without its logits; rope: rope_config(head_dim, ...) for a scaled context."""
         self.cfg = dict(cfg)
         self.ccfg = make_config(cfg, mode, n_layer_buffers, max_tokens, device, source, stack_path)
         self.device = torch.device("cuda", device)
         self._allocator = _TorchAllocator(device) if torch_alloc else None
         h = c_void_p()
-        check(lib.soup_model_create(byref(self.ccfg), byref(self._allocator.struct) if self._allocator else None,
-                                    byref(h)))
+        options = _lib.ModelOptions(1 if loss_in_pieces else 0, ctypes.addressof(rope) if rope is not None else None)
+        check(lib.soup_model_create_with(byref(self.ccfg), byref(options),
+                                         byref(self._allocator.struct) if self._allocator else None, byref(h)))
         self.h = h
         self.blob_bytes = blob_bytes(cfg)
         self._keep = {}
@@ -155,11 +158,20 @@ class SoupModel:
         self._keep["head"] = (embed, final_gamma, lm_head)
         self._ck(lib.soup_model_set_head(self.h, _ptr(embed), _ptr(final_gamma), _ptr(lm_head)))
 
-    def set_lora(self, params: torch.Tensor):
-        """params: flat fp32 cuda tensor of lora_numel elements (layout of include/soup.h)."""
+    def set_lora(self, params: torch.Tensor, adam_bits: int = 32):
+        """params: flat fp32 cuda tensor of lora_numel elements (layout of include/soup.h).  adam_bits = 8:
+        optimizer states of 8 bits (adamw_state's, a layer a tensor)."""
         assert params.numel() == self.lora_n and params.dtype == torch.float32 and params.is_cuda
         self.lora_params = params
         self.lora_grads = torch.zeros_like(params)
+        if adam_bits != 32:
+            layers = self.cfg["n_layers"]
+            state = adamw_state([self.lora_n // layers] * layers, adam_bits, params.device)
+            self.adam_m, self.adam_v = state["m"], state["v"]
+            self.adam_m_scale, self.adam_v_scale = state["m_scale"], state["v_scale"]
+            self._ck(lib.soup_model_set_lora_adam8(self.h, _ptr(self.lora_params), _ptr(self.lora_grads), _ptr(self.adam_m),
+                                                   _ptr(self.adam_v), _ptr(self.adam_m_scale), _ptr(self.adam_v_scale)))
+            return
         self.adam_m = torch.zeros_like(params)
         self.adam_v = torch.zeros_like(params)
         self._ck(lib.soup_model_set_lora(self.h, _ptr(self.lora_params), _ptr(self.lora_grads), _ptr(self.adam_m),

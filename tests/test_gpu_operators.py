@@ -12,6 +12,15 @@ pytestmark = pytest.mark.gpu
 BF16 = 2.0 ** -8  # one rounding to bf16, relative to the value
 
 
+@pytest.fixture(autouse=True)
+def fp32_by_default():
+    """Inputs are drawn in fp32 whatever another test module has set."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
 def gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 

@@ -1,0 +1,206 @@
+"""The training step with the loss in pieces of the vocabulary, scaled rotary positions and 8-bit optimizer
+states: each against the float64 oracle or the plain path, and all together as a long-context run has
+them.  Bounds on losses and gradients are those of the plain step's own parity tests; where two paths of the
+library share everything up to one operator, what that operator may add is derived beside the check."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import model as om
+from oracle import pref
+from tests.gpu_util import Pair, cosine, rel_err
+
+pytestmark = pytest.mark.gpu
+
+PRE = 64
+CFG = dict(synth.TINY, seq=192)
+ROWS = 4 * 192
+
+
+@pytest.fixture(scope="module")
+def pair():
+    p = Pair(CFG, seed=61, modes=("streamed",), max_tokens=ROWS)
+    yield p
+    p.close()
+
+
+def model(pair, mode="streamed", adam_bits=32, **options):
+    from layer_streamed_nf4_lut_b200.model import SoupModel
+    gm = SoupModel(pair.cfg, mode=mode, max_tokens=ROWS, **options)
+    for i in range(pair.cfg["n_layers"]):
+        gm.load_layer_nf4(i, pair.models["streamed"].read_layer_nf4(i))
+    gm.set_head(*pair.head_t)
+    gm.set_lora(pair.params_t.clone(), adam_bits)
+    return gm
+
+
+def check_grads(pair, gm, og, bound=0.999):
+    pair.models["other"] = gm
+    try:
+        g = pair.gpu_grads("other")
+    finally:
+        del pair.models["other"]
+    worst = min(min(cosine(gA, og[k][0]), cosine(gB, og[k][1])) for k, (gA, gB) in g.items())
+    assert worst > bound, worst
+
+
+@pytest.fixture(scope="module")
+def pieces(pair):
+    gm = model(pair, loss_in_pieces=True)
+    yield gm
+    gm.close()
+
+
+@pytest.mark.parametrize("batch,masked", [(1, False), (3, True)])
+def test_sft_in_pieces(pair, pieces, batch, masked):
+    cfg = dict(CFG, batch=batch)
+    ids = synth.token_batch(cfg, 62)
+    mask = synth.last_half_mask(batch, cfg["seq"]) if masked else None
+    loss = pieces.step(ids, mask=mask, apply_optimizer=False)
+    ol, og, _ = om.sft_step(cfg, pair.olayers, pair.olora, pair.ohead, ids, mask)
+    assert abs(loss - ol) / abs(ol) < 1e-2
+    check_grads(pair, pieces, og)
+    # the two paths read the same bf16 rows: a logit is off by (256 / 16 + 16) 2^-23 sum |h w| in each, the sum
+    # being below 8 (256 values of about 0.8 times 0.016), its exponential and log by 2^-21 (1 + 16)
+    plain = pair.models["streamed"].step(ids, mask=mask, apply_optimizer=False)
+    assert abs(loss - plain) <= 2 * (32 * 2.0 ** -23 * 8 + 17 * 2.0 ** -21)
+
+
+def test_every_target_masked(pair, pieces):
+    ids = synth.token_batch(dict(CFG, batch=2), 63)
+    mask = np.zeros((2, CFG["seq"]), np.uint8)
+    loss = pieces.step(ids, mask=mask, apply_optimizer=False)
+    plain = pair.models["streamed"].step(ids, mask=mask, apply_optimizer=False)
+    assert loss == plain or (np.isnan(loss) and np.isnan(plain))
+    assert (pieces.lora_grads == 0).all()
+
+
+@pytest.mark.parametrize("share,together", [(False, False), (False, True), (True, False), (True, True)])
+def test_dpo_in_pieces(pair, pieces, share, together):
+    ids = synth.preference_batch(dict(CFG, batch=4, n_pairs=2, prefix_len=PRE), 64)
+    kw = dict(loss="dpo", n_pairs=2, prefix_len=PRE, beta=0.1, apply_optimizer=False, share_prefix=share,
+              dpo_shared_load=together)
+    loss = pieces.step(torch.from_numpy(ids).cuda(), **kw)
+    pi, ref = pieces.last_logps(4)
+    ol, og, aux = om.dpo_step(dict(CFG, batch=4), pair.olayers, pair.olora, pair.ohead, ids, PRE, 0.1)
+    assert rel_err(pi, aux["pi"]) < 1e-2 and rel_err(ref, aux["ref"]) < 1e-2
+    closed, _ = om.dpo_loss(pi.astype(np.float64), ref.astype(np.float64), 0.1)
+    assert abs(loss - closed) < 1e-5 and abs(loss - ol) < 1e-2 * abs(ol)
+    check_grads(pair, pieces, og)
+
+
+@pytest.mark.parametrize("kind", ["simpo", "orpo", "kto"])
+def test_preference_losses_in_pieces(pair, pieces, kind):
+    ids = synth.preference_batch(dict(CFG, batch=4, n_pairs=2, prefix_len=PRE), 65)
+    hp = dict(simpo=dict(beta=2.0, gamma=0.5), orpo=dict(lam=0.1), kto=dict(beta=0.1, lam_d=1.0, lam_u=1.33))[kind]
+    labels = np.array([1, 0, 0, 1], np.uint8)
+    kw = dict(simpo=dict(beta=2.0, gamma=0.5), orpo=dict(lambda_or=0.1),
+              kto=dict(beta=0.1, lambda_d=1.0, lambda_u=1.33, labels=labels))[kind]
+    loss = pieces.step(torch.from_numpy(ids).cuda(), loss=kind, n_pairs=2, prefix_len=PRE, apply_optimizer=False, **kw)
+    ol, og, aux = pref.pref_step(dict(CFG, batch=4), pair.olayers, pair.olora, pair.ohead, ids, PRE, kind, hp, labels)
+    assert rel_err(pieces.last_logps(4)[0], aux["pi"]) < 1e-2
+    assert abs(loss - ol) < 1e-2 * abs(ol)
+    check_grads(pair, pieces, og)
+
+
+def test_no_logits_are_held(pair, pieces):
+    gm = model(pair)  # loaded like the other (the pair's own also holds the quantiser's scratch)
+    plain = gm.stats()["device_bytes"]
+    gm.close()
+    rows = ROWS * CFG["vocab"] * 6
+    assert rows > 4 << 20
+    # at this vocabulary the pieces' own workspace is not small; at the 8B shape's it is
+    from layer_streamed_nf4_lut_b200 import _lib
+    import ctypes
+    need, most = ctypes.c_size_t(), 0
+    for t in range(256, ROWS + 1, 256):
+        assert _lib.lib.soup_linear_ce_workspace(t, CFG["hidden"], CFG["vocab"], 1, ctypes.byref(need)) == 0
+        most = max(most, need.value)
+    assert abs(pieces.stats()["device_bytes"] - (plain - rows + most + 4 * ROWS)) <= 1024
+
+
+@pytest.mark.parametrize("scaling,kw", [("none", {}), ("linear", dict(factor=4.0)), ("ntk", dict(factor=4.0)),
+                                        ("llama3", dict(factor=8.0, original_len=64)),
+                                        ("yarn", dict(factor=8.0, original_len=64, high_freq_factor=32.0))])
+def test_scaled_positions(pair, monkeypatch, scaling, kw):
+    from layer_streamed_nf4_lut_b200 import model as M
+    rope = M.rope_config(CFG["head_dim"], CFG["rope_theta"], scaling=scaling, **kw)
+    freq, grow = M.rope_frequencies(rope)
+
+    def tables(S, d, theta):
+        ang = np.arange(S, dtype=np.float64)[:, None] * freq[None, :]
+        return grow * np.cos(ang), grow * np.sin(ang)
+
+    monkeypatch.setattr(om, "rope_tables", tables)
+    gm = model(pair, rope=rope)
+    try:
+        ids = synth.token_batch(dict(CFG, batch=1), 66)
+        loss = gm.step(ids, apply_optimizer=False)
+        ol, og, _ = om.sft_step(dict(CFG, batch=1), pair.olayers, pair.olora, pair.ohead, ids)
+        assert abs(loss - ol) / abs(ol) < 1e-2
+        check_grads(pair, gm, og)
+        if scaling == "none":  # the same tables as the plain model's
+            assert loss == pair.models["streamed"].step(ids, apply_optimizer=False)
+            assert torch.equal(gm.lora_grads, pair.models["streamed"].lora_grads)
+    finally:
+        gm.close()
+
+
+def slices(gm, flat):
+    return list(flat.split(gm.lora_n // gm.cfg["n_layers"]))
+
+
+@pytest.mark.parametrize("within", [True, False])
+def test_8_bit_states_in_the_step(pair, within):
+    """The step's updates are adamw_multi's on the same gradients, the states bit for bit, whether they run
+    inside the backward pass (eager, then replayed from graphs) or after it."""
+    from layer_streamed_nf4_lut_b200 import model as M
+    gm = model(pair, adam_bits=8)
+    try:
+        ids = torch.from_numpy(synth.token_batch(dict(CFG, batch=2), 67)).cuda()
+        p = gm.lora_params.clone()
+        state = M.adamw_state([gm.lora_n // CFG["n_layers"]] * CFG["n_layers"], 8)
+        for step in range(1, 6):
+            lr = 1e-3 / step
+            if within:
+                gm.step(ids, lr=lr)
+            else:
+                gm.step(ids, apply_optimizer=False)
+                gm.optimizer_step(lr)
+            # the step's betas are fp32 numbers
+            M.adamw_multi(slices(gm, p), slices(gm, gm.lora_grads), lr=lr, step=step,
+                          betas=(float(np.float32(0.9)), float(np.float32(0.999))), eps=float(np.float32(1e-8)), **state)
+            torch.cuda.synchronize()
+            # the step's corrections and lr are rounded to fp32 before the call's: steps of about lr, below 10 lr
+            assert ((gm.lora_params - p).abs() <= 10 * lr * 2.0 ** -21 + 2.0 ** -23 * p.abs()).all()
+            p.copy_(gm.lora_params)
+            assert torch.equal(gm.adam_m, state["m"]) and torch.equal(gm.adam_v, state["v"])
+            assert torch.equal(gm.adam_m_scale, state["m_scale"]) and torch.equal(gm.adam_v_scale, state["v_scale"])
+    finally:
+        gm.close()
+
+
+def test_a_long_context_run_with_all_of_them(pair):
+    """Scaled positions -> loss in pieces -> 8-bit AdamW, several steps, streamed and resident: the same bits, and
+    the parameters close to those of the plain step under 32-bit states."""
+    from layer_streamed_nf4_lut_b200 import model as M
+    rope = M.rope_config(CFG["head_dim"], CFG["rope_theta"], scaling="yarn", factor=8.0, original_len=64, high_freq_factor=32.0)
+    ids = torch.from_numpy(synth.token_batch(dict(CFG, batch=2), 68)).cuda()
+    mask = torch.from_numpy(synth.last_half_mask(2, CFG["seq"])).cuda()
+    got = {}
+    for name, mode, bits, options in (("streamed", "streamed", 8, dict(loss_in_pieces=True, rope=rope)),
+                                      ("resident", "resident", 8, dict(loss_in_pieces=True, rope=rope)),
+                                      ("plain", "streamed", 32, dict(rope=rope))):
+        gm = model(pair, mode, bits, **options)
+        try:
+            losses = [gm.step(ids, mask=mask, lr=1e-3) for _ in range(5)]
+            torch.cuda.synchronize()
+            got[name] = (losses, gm.lora_params.clone())
+        finally:
+            gm.close()
+    assert got["streamed"][0] == got["resident"][0] and torch.equal(got["streamed"][1], got["resident"][1])
+    moved, plain = got["streamed"][1] - pair.params_t, got["plain"][1] - pair.params_t
+    assert torch.isfinite(moved).all()
+    assert abs(got["streamed"][0][0] - got["plain"][0][0]) <= 2 * (32 * 2.0 ** -23 * 8 + 17 * 2.0 ** -21)
+    assert cosine(moved.double().cpu().numpy(), plain.double().cpu().numpy()) > 0.99

@@ -188,3 +188,27 @@ def test_rope_refusals(kw, status):
     c = ctypes.byref(M.rope_config(a["rot"])) if a["rot"] else None
     assert L.soup_rope(c, a["q"], a["ldq"], a["qo"], a["ldqo"], a["hq"], a["k"], a["ldk"], a["ko"], a["ldko"], a["hk"], a["d"],
                        a["T"], a["pos"], a["dtype"], 0, None) == status
+
+
+# ------------------------------------------------------------------ the model's use of them
+def test_model_options():
+    import synth
+    cfg, out = M.make_config(synth.TINY), ctypes.c_void_p()
+    n = ctypes.c_size_t()
+    assert L.soup_lora_state_numel(ctypes.byref(cfg), ctypes.byref(n)) == OK
+    per_layer = M.lora_numel(synth.TINY) // synth.TINY["n_layers"]
+    assert n.value == synth.TINY["n_layers"] * (-(-per_layer // 256) * 256)
+    assert L.soup_lora_state_numel(None, ctypes.byref(n)) == INVALID and L.soup_lora_state_numel(ctypes.byref(cfg), None) == INVALID
+
+    def create(rope=None, pieces=0, cfg=cfg):  # all refused before a device is touched
+        o = _lib.ModelOptions(pieces, ctypes.addressof(rope) if rope is not None else None)
+        return L.soup_model_create_with(ctypes.byref(cfg), ctypes.byref(o), None, ctypes.byref(out))
+    assert create(M.rope_config(32)) == UNSUPPORTED  # part of a head
+    assert create(M.rope_config(64, interleaved=True)) == UNSUPPORTED
+    assert create(M.rope_config(64, theta=0.5)) == INVALID
+    assert create(M.rope_config(64, scaling="linear", factor=0.5)) == INVALID
+    assert create(pieces=1, cfg=M.make_config(dict(synth.TINY, vocab=(1 << 22) + 4))) == UNSUPPORTED
+    assert create(pieces=1, cfg=M.make_config(dict(synth.TINY), max_tokens=1 << 24)) == UNSUPPORTED
+    assert L.soup_model_create_with(None, None, None, ctypes.byref(out)) == INVALID
+    f = L.soup_model_set_lora_adam8
+    assert f(None, A, A, A, A, A, A) == INVALID
