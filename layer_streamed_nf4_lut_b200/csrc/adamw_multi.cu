@@ -93,28 +93,38 @@ __device__ __forceinline__ float byte_value(uint32_t w, int j, float zero) {  //
   return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650u | j)) - (8388608.f + zero);
 }
 __device__ __forceinline__ uint32_t rounded(float x) { return __float_as_uint(x + 12582912.f); }  // low byte, |x| < 2^21
+__device__ __forceinline__ float rounded_value(uint32_t r) { return __uint_as_float(r) - 12582912.f; }
 __device__ __forceinline__ uint32_t low_bytes(const uint32_t* w) {
   return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
 }
+// q / 127 and q / 255, correctly rounded for every code: the product with the reciprocal, corrected by the
+// remainder (Markstein 1990).
+template <int D>
+__device__ __forceinline__ float code_share(float q) {
+  constexpr float inv = 1.f / D;
+  const float r = __fmul_rn(q, inv);
+  return __fmaf_rn(__fmaf_rn(-static_cast<float>(D), r, q), inv, r);
+}
 __device__ __forceinline__ void m_values(uint2 q, float scale, float (&m)[8]) {
   const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};  // -127 .. 127 as 1 .. 255
-  const float k = scale * (1.f / 16129.f);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float r = byte_value(w[j >> 2], j & 3, 128.f);
-    m[j] = r * fabsf(r) * k;
+    const float r = code_share<127>(byte_value(w[j >> 2], j & 3, 128.f));
+    m[j] = __fmul_rn(__fmul_rn(r, fabsf(r)), scale);
   }
 }
 __device__ __forceinline__ void v_values(uint2 q, float scale, float (&v)[8]) {
   const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float r = byte_value(w[j >> 2], j & 3, 0.f), r2 = r * r * (1.f / 65025.f);
-    v[j] = r2 * r2 * scale;
+    const float r = code_share<255>(byte_value(w[j >> 2], j & 3, 0.f)), r2 = __fmul_rn(r, r);
+    v[j] = __fmul_rn(__fmul_rn(r2, r2), scale);
   }
 }
-// Square root and reciprocal to about 2^-22: the step they make is lr times a number near 1, and a code
-// is 8 bits, while the correctly rounded forms make the 8-bit kernel bound by its arithmetic.
+// Square root and reciprocal to about 2^-22, while the correctly rounded forms make the 8-bit kernel bound by
+// its arithmetic: enough for the step, lr times a number near 1.  A code that they leave in doubt, next to the
+// border of two, is formed again with every operation rounded correctly: a code is a step of 1.6 % of m or v,
+// and which of two it is does not hang on an approximation.
 __device__ __forceinline__ float root(float x) {
   float y;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -218,8 +228,8 @@ __global__ void __launch_bounds__(32 * WARPS, BITS8 ? 5 : 4) adamw_multi_kernel(
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    m[j] = k.b1 * m[j] + k.g1 * gv[j];
-    v[j] = k.b2 * v[j] + k.g2 * gv[j] * gv[j];
+    m[j] = __fadd_rn(__fmul_rn(k.b1, m[j]), __fmul_rn(k.g1, gv[j]));
+    v[j] = __fadd_rn(__fmul_rn(k.b2, v[j]), __fmul_rn(__fmul_rn(k.g2, gv[j]), gv[j]));
     // bc2 carries 2^24: the root takes no subnormal numbers
     const float under = root(v[j] * k.bc2) * 0x1p-12f + k.eps;
     pv[j] = pv[j] - k.lr * (m[j] * k.bc1 * reciprocal(under) + k.wd * pv[j]);
@@ -249,12 +259,28 @@ __global__ void __launch_bounds__(32 * WARPS, BITS8 ? 5 : 4) adamw_multi_kernel(
     // 127 sqrt(m / ms) = sqrt(127^2 m / ms), 255 (v / vs)^(1/4) = sqrt(sqrt(255^4 v / vs))
     const float mr = ms > 0.f ? 127.f * 127.f / ms : 0.f, vr = vs > 0.f ? 255.f * 255.f * 255.f * 255.f / vs : 0.f;
     uint32_t mo[8], vo[8];
+    float m_off = 0.f, v_off = 0.f;  // furthest from a whole number
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      mo[j] = rounded(copysignf(root(fabsf(m[j]) * mr), m[j]));
+      const float x = copysignf(root(fabsf(m[j]) * mr), m[j]);
       float u = root(root(v[j] * vr));
       if (v[j] > 0.f) u = fmaxf(u, 1.f);
+      mo[j] = rounded(x);
       vo[j] = rounded(u);
+      m_off = fmaxf(m_off, fabsf(x - rounded_value(mo[j])));
+      v_off = fmaxf(v_off, fabsf(u - rounded_value(vo[j])));
+    }
+    // Approximate and correctly rounded values are within 127 (1.5 2^-23 + 2.5 2^-24) = 4.2e-5 of each other
+    // for m, within 255 (1.75 2^-23 + 2.75 2^-24) = 9.5e-5 for v: one warp in 13 has a value that near to a border.
+    if (__any_sync(0xffffffffu, m_off > 0.5f - 5e-5f || v_off > 0.5f - 1e-4f)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = ms > 0.f ? __fmul_rn(127.f, __fsqrt_rn(__fdiv_rn(fabsf(m[j]), ms))) : 0.f;
+        float u = vs > 0.f ? __fmul_rn(255.f, __fsqrt_rn(__fsqrt_rn(__fdiv_rn(v[j], vs)))) : 0.f;
+        if (v[j] > 0.f) u = fmaxf(u, 1.f);
+        mo[j] = rounded(copysignf(x, m[j]));
+        vo[j] = rounded(u);
+      }
     }
     mq = make_uint2(low_bytes(mo), low_bytes(mo + 4));
     vq = make_uint2(low_bytes(vo), low_bytes(vo + 4));

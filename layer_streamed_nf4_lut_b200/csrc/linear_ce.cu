@@ -36,6 +36,7 @@ constexpr int TILE = 256;            // rows and columns of a CTA pair's output 
 constexpr int GROUP = TILE / 2;      // columns a group of four epilogue warps works through
 constexpr int BK = 64;               // k-block: 64 bf16 = one 128-byte swizzle row
 constexpr int STAGES = 6;            // operand ring
+constexpr int CHUNK = 16;            // k-blocks of a logit that one accumulator adds up (see ce_gemm_kernel)
 constexpr int OPERAND = 128 * 128;   // bytes of one operand's k-block in one CTA (128 rows x 64 bf16)
 constexpr int STAGE_BYTES = 2 * OPERAND;
 constexpr int STAGING = 2 * 16384;   // epilogue: a box of 128 rows x 128 bytes for each group of four warps
@@ -72,6 +73,27 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
+}
+// mbar_wait_bounded by a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (;;) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const bool late = globaltimer_ns() - t0 > WAIT_LIMIT_NS;
+    if (!__any_sync(0xffffffffu, late || *abort_flag)) continue;
+    if (late) {
+      *abort_flag = 1;
+      set_dev_error(err, DEVERR_TIMEOUT);
+    }
+    __syncwarp();
+    return false;
+  }
 }
 // Barrier of the eight epilogue warps, telling each thread whether all of them have `ok`: a wait that
 // gave up in one thread ends the loop for all, so that none is left alone at a barrier.
@@ -138,6 +160,11 @@ __device__ __forceinline__ Unit unit_of(const CeGemm& p, int m_tiles, int splits
 // 256 x 256 tiles, one CTA pair each (tcgen05 cta_group::2, M = 256, N = 256), two accumulators
 // in tensor memory so that a tile's epilogue runs beside the next tile's products.
 // GRAD = false: logits tile -> P, sums.  GRAD = true: P W -> accumulator of the tile's share.
+//
+// A logit is added up in chunks of 1024 products, by turns in the two accumulators, and the chunks in the
+// epilogue's registers: the tensor cores cut off what falls below an accumulator's last bit, and over
+// 8192 products these cuts, all towards zero, moved a row's lse by 1.9e-5 (1.4e-6 of it), four times
+// what fp32 sums give.  It also frees an accumulator as soon as it is read, before the exponentials.
 template <bool GRAD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_kernel(const __grid_constant__ CeGemm p) {
   extern __shared__ uint8_t smem_raw[];
@@ -183,54 +210,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
   const int splits = GRAD ? grad_splits(m_tiles, p.cols, pairs, p.kb_first) : 1;
   const int units = m_tiles * p.n_tiles * splits;
 
-  if (warp == 0 && lane == 0) {
+  // The two issuing warps run their loops whole, with one lane elected for what is issued: descriptors and
+  // coordinates then stay in uniform registers.  From a branch of one lane each instruction first had
+  // to move them there, and the tensor cores waited for it: 6 % at 2048 x 8192 x 128256.
+  if (warp == 0) {
     // ---- operand loads: this CTA's 128 rows of A and its half of B's 256 columns
-    int it = 0;
+    const bool issues = elect_one();
+    uint32_t s = 0, phase = 1;  // of an empty ring: each stage's first wait is over at once
     for (int u = pair; u < units; u += pairs) {
       const Unit t = unit_of<GRAD>(p, m_tiles, splits, u);
-      if (t.kb_lo == t.kb_hi) continue;
       const int m0 = t.m * TILE + rank * 128, n0 = t.n * TILE + rank * 128;
-      for (int kb = t.kb_lo; kb < t.kb_hi; ++kb, ++it) {
-        const int s = it % STAGES;
-        if (it >= STAGES && !mbar_wait_bounded(&empty[s], ((it / STAGES) - 1) & 1, abort_flag, p.err)) goto done;
-        uint8_t* a = smem + s * STAGE_BYTES;
-        uint8_t* b = a + OPERAND;
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
-        const uint32_t bar = cluster_addr(&full[s], 0);
-        tma_load_2d_pair(a, &p.ta, kb * BK, m0, bar);
-        if (GRAD) {
-          tma_load_2d_pair(b, &p.tb, n0, p.w_row0 + kb * BK, bar);
-          tma_load_2d_pair(b + 8192, &p.tb, n0 + 64, p.w_row0 + kb * BK, bar);
-        } else {
-          tma_load_2d_pair(b, &p.tb, kb * BK, p.w_row0 + n0, bar);
+      for (int kb = t.kb_lo; kb < t.kb_hi; ++kb) {
+        if (!mbar_wait_warp(&empty[s], phase, abort_flag, p.err)) goto done;
+        if (issues) {
+          uint8_t* a = smem + s * STAGE_BYTES;
+          uint8_t* b = a + OPERAND;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
+          const uint32_t bar = cluster_addr(&full[s], 0);
+          tma_load_2d_pair(a, &p.ta, kb * BK, m0, bar);
+          if (GRAD) {
+            tma_load_2d_pair(b, &p.tb, n0, p.w_row0 + kb * BK, bar);
+            tma_load_2d_pair(b + 8192, &p.tb, n0 + 64, p.w_row0 + kb * BK, bar);
+          } else {
+            tma_load_2d_pair(b, &p.tb, kb * BK, p.w_row0 + n0, bar);
+          }
+        }
+        __syncwarp();
+        if (++s == STAGES) {
+          s = 0;
+          phase ^= 1;
         }
       }
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ---- products of both CTAs
-    const uint32_t idesc = idesc_bf16(TILE, TILE, false, GRAD);
-    int it = 0, n_done = 0;
+    const bool issues = elect_one();
+    const uint32_t idesc = idesc_bf16(TILE, TILE, false, GRAD), base = smem_u32(smem);
+    const uint64_t da0 = sw128_kmajor_desc(base);
+    const uint64_t db0 = GRAD ? sw128_mnmajor_desc(base + OPERAND) : sw128_kmajor_desc(base + OPERAND);
+    uint32_t s = 0, phase = 0, b = 0, b_phase = 1;
     for (int u = pair; u < units; u += pairs) {
       const Unit t = unit_of<GRAD>(p, m_tiles, splits, u);
-      if (t.kb_lo == t.kb_hi) continue;
-      const int b = n_done & 1;
-      // an accumulator's first products wait until its last ones have been read out
-      if (n_done >= 2 && !mbar_wait_bounded(&acc_empty[b], ((n_done >> 1) - 1) & 1, abort_flag, p.err)) goto done;
-      for (int kb = t.kb_lo; kb < t.kb_hi; ++kb, ++it) {
-        const int s = it % STAGES;
-        if (!mbar_wait_bounded(&full[s], (it / STAGES) & 1, abort_flag, p.err)) goto done;
-        tc_fence_after();
-        const uint32_t a = smem_u32(smem + s * STAGE_BYTES);
-        const uint64_t da = sw128_kmajor_desc(a);
-        const uint64_t db = GRAD ? sw128_mnmajor_desc(a + OPERAND) : sw128_kmajor_desc(a + OPERAND);
+      for (int kb = t.kb_lo; kb < t.kb_hi;) {
+        const int stop = GRAD ? t.kb_hi : min(t.kb_hi, kb + CHUNK);
+        // an accumulator's first products wait until its last ones have been read out
+        if (!mbar_wait_warp(&acc_empty[b], b_phase, abort_flag, p.err)) goto done;
+        uint32_t more = 0;
+        for (; kb < stop; ++kb) {
+          if (!mbar_wait_warp(&full[s], phase, abort_flag, p.err)) goto done;
+          tc_fence_after();
+          if (issues) {
+            const uint64_t da = da0 + s * (STAGE_BYTES >> 4), db = db0 + s * (STAGE_BYTES >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma_f16_pair(tmem + b * TILE, da + k * (32 >> 4), db + k * ((GRAD ? 2048 : 32) >> 4), idesc,
-                          (kb > t.kb_lo || k > 0) ? 1u : 0u);
-        tc_commit_pair(&empty[s]);
+            for (int k = 0; k < 4; ++k) {
+              tc_mma_f16_pair(tmem + b * TILE, da + k * (32 >> 4), db + k * ((GRAD ? 2048 : 32) >> 4), idesc, more);
+              more = 1;
+            }
+            tc_commit_pair(&empty[s]);
+          }
+          __syncwarp();
+          more = 1;
+          if (++s == STAGES) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (issues) tc_commit_pair(&acc_full[b]);
+        __syncwarp();
+        b ^= 1;
+        if (b == 0) b_phase ^= 1;
       }
-      tc_commit_pair(&acc_full[b]);
-      ++n_done;
     }
   } else if (warp >= 4) {
     // ---- epilogue: thread = accumulator row; two groups of four warps take half of the columns each
@@ -240,17 +289,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
     uint8_t* box = staging + group * 16384;
     uint8_t* my_row = box + row * 128;
     const bool elected = (threadIdx.x & 127) == 0;
-    int n_done = 0;
+    int n_done = 0, turn = 0;
     for (int u = pair; u < units; u += pairs) {
       const Unit t = unit_of<GRAD>(p, m_tiles, splits, u);
       if (t.kb_lo == t.kb_hi) continue;
       const int m0 = t.m * TILE + rank * 128;
-      const int buf = n_done & 1;
       const int n0 = t.n * TILE + group * GROUP;  // this group's first column
-      if (!epilogue_all(mbar_wait_bounded(&acc_full[buf], (n_done >> 1) & 1, abort_flag, p.err))) goto done;
-      tc_fence_after();
-      const uint32_t acc = tmem + lanes + buf * TILE + group * GROUP;
       if (GRAD) {
+        const int buf = n_done & 1;
+        if (!epilogue_all(mbar_wait_bounded(&acc_full[buf], (n_done >> 1) & 1, abort_flag, p.err))) goto done;
+        tc_fence_after();
+        const uint32_t acc = tmem + lanes + buf * TILE + group * GROUP;
         const int out_row = (t.share * m_tiles + t.m) * TILE + rank * 128;
         for (int c = 0; c < GROUP; c += 32) {
           uint32_t v[32];
@@ -272,38 +321,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
             tma_store_commit();
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+        ++n_done;
       } else {
+        float l[GROUP];  // this thread's logits
+        for (int kb = 0; kb < p.kb; kb += CHUNK) {
+          const int buf = n_done & 1;
+          if (!epilogue_all(mbar_wait_bounded(&acc_full[buf], (n_done >> 1) & 1, abort_flag, p.err))) goto done;
+          tc_fence_after();
+          const uint32_t acc = tmem + lanes + buf * TILE + group * GROUP;
+#pragma unroll
+          for (int c = 0; c < GROUP; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(acc + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) l[c + j] = (kb ? l[c + j] : 0.f) + __uint_as_float(v[j]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
+          ++n_done;
+        }
         const int r = m0 + row;
         const bool live = r < rows;
         const int2 tg = live ? p.target[r] : make_int2(-1, -1);
         const int ta = tg.x - p.w_row0 - n0, tb = tg.y - p.w_row0 - n0;  // the targets' columns here
         const int valid = p.cols - n0;                                    // columns inside the vocabulary
+        // columns that stay out: the targets', for the few rows that have one here, and those past the end
+        if (__any_sync(0xffffffffu, (ta >= 0 && ta < GROUP) || (tb >= 0 && tb < GROUP)) || valid < GROUP) {
+#pragma unroll
+          for (int j = 0; j < GROUP; ++j)
+            if (j == ta || j == tb || j >= valid) l[j] = -INFINITY;
+        }
         float ref = live ? p.ref[r] : 0.f, total = 0.f;
         for (int attempt = 0; attempt < 2; ++attempt) {
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
           for (int c = 0; c < GROUP; c += 64) {
             uint32_t w[32];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t v[32];
-              const int c1 = c + 32 * half;
-              tmem_ld32(acc + c1, v);
-              tmem_ld_wait();
-              // columns that stay out: the targets', for the few rows that have one here, and those past the end
-              const int a = ta - c1, b = tb - c1;
-              if (__any_sync(0xffffffffu, (a >= 0 && a < 32) || (b >= 0 && b < 32)) || c1 + 32 > valid) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (j == a || j == b || c1 + j >= valid) v[j] = 0xff800000u;  // -inf
-              }
-#pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                const float e0 = exp2_approx(fmaf(__uint_as_float(v[j]), LOG2E, -ref));
-                const float e1 = exp2_approx(fmaf(__uint_as_float(v[j + 1]), LOG2E, -ref));
-                sum[j & 3] += e0;
-                sum[(j + 1) & 3] += e1;
-                w[16 * half + (j >> 1)] = pack_bf16x2(e0, e1);
-              }
+            for (int j = 0; j < 64; j += 2) {
+              const float e0 = exp2_approx(fmaf(l[c + j], LOG2E, -ref));
+              const float e1 = exp2_approx(fmaf(l[c + j + 1], LOG2E, -ref));
+              sum[j & 3] += e0;
+              sum[(j + 1) & 3] += e1;
+              w[j >> 1] = pack_bf16x2(e0, e1);
             }
             if (p.store_p) {
               if (elected) tma_store_wait_read<0>();
@@ -323,21 +388,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
           total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
           // A logit far above ref (an infinite sum counts): once more, against the row's largest logit here
           const bool over = live && total > REF_ROOM;
-          float* theirs = join + 128 * buf + row;  // one for each accumulator
+          float* theirs = join + 128 * (turn & 1) + row;  // by turns: the first group reads one while the other is written
           if (group == 1) *theirs = total;
           if (epilogue_all(!over) || attempt == 1) {
             if (group == 0) total += *theirs;
             break;
           }
           float top = -INFINITY;
-          for (int c = 0; c < GROUP; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(acc + c, v);
-            tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j != ta && c + j != tb && c + j < valid) top = fmaxf(top, __uint_as_float(v[j]));
-          }
+          for (int j = 0; j < GROUP; ++j) top = fmaxf(top, l[j]);
           if (elected) tma_store_wait_all();  // the boxes are written again, here and below: in order
           group_sync(group);
           *reinterpret_cast<float2*>(my_row) = make_float2(top, over ? 1.f : 0.f);
@@ -349,16 +408,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
             *p.raised = 1;
           }
         }
+        ++turn;
         if (group == 0) {
           const long long at = static_cast<long long>(p.tile0 + t.n) * p.tcap + r;
           p.part_s[at] = total;
           p.part_r[at] = ref;
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
-      ++n_done;
     }
     if (elected) tma_store_wait_all();
   }
