@@ -12,7 +12,7 @@
 //
 // Bound by HBM: p is read and written, g read, the states read and written: 28 B per element with
 // fp32 throughout, 16 B with 8-bit states.  A warp works one block (8 elements a lane), so a scale
-// is one warp reduction, and finds its tensor by halving.  A warp for each block, taken up in order by the
+// is one warp reduction, and finds its tensor from a short table.  A warp for each block, taken up in order by the
 // hardware, measured better than persistent warps with runs of 1 to 70 blocks (what is in flight then lies
 // together, which keeps DRAM pages open): 674 against 697 to 830 us at 168 M elements with fp32 throughout
 // (6.97 TB/s), 450 us (5.98 TB/s) with 8-bit states, where the arithmetic of the codes comes near to the
@@ -29,14 +29,14 @@ namespace {
 
 constexpr int BLOCK = ADAMW_BLOCK;
 constexpr int WARPS = 8;              // of a thread block; a warp works one block of elements at a time
+constexpr int NEAR = 1024;            // entries of the look-up of a block's tensor
 constexpr int LAUNCH_TENSORS = 640;  // descriptors of one launch: 32 KB of kernel parameters hold 800
 
 struct AdamTensor {
   void* p;
   const void* g;
   uint16_t* pb;
-  long long n;
-  int aligned;  // p, g and pb for 8 elements in one access
+  long long n2;  // twice its elements, plus 1 where p, g and pb are aligned for 8 elements in one access
 };
 struct Hyper {
   float lr, b1, b2, g1, g2, eps, wd, bc1, bc2;  // g = 1 - b
@@ -47,10 +47,11 @@ struct AdamArgs {
   const float* hp;
   Hyper k;
   int count;
-  int search;            // first step of the look-up of a block's tensor
+  int near_shift;
+  uint16_t hint[NEAR];   // the tensor of every 2^near_shift-th block
   long long blocks;      // of this launch
   long long block0;      // state block of this launch's first
-  long long first[LAUNCH_TENSORS];  // first block of each tensor, from this launch's first
+  long long first[LAUNCH_TENSORS + 1];  // first block of each tensor, from this launch's first
   AdamTensor t[LAUNCH_TENSORS];
 };
 
@@ -148,11 +149,21 @@ __device__ __forceinline__ float block_top(const float (&x)[8]) {
 // (j * 32 + lane), and shared memory turns them into 8 a lane and back.
 template <typename E>
 __device__ __forceinline__ void load_strided(const E* p, int n, int lane, float (&v)[8]) {
+  if (n == BLOCK) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = load_f(p + j * 32 + lane);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = j * 32 + lane < n ? load_f(p + j * 32 + lane) : 0.f;
 }
 template <typename E>
 __device__ __forceinline__ void store_strided(E* p, int n, int lane, const float (&v)[8]) {
+  if (n == BLOCK) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) store_f(p + j * 32 + lane, v[j]);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     if (j * 32 + lane < n) store_f(p + j * 32 + lane, v[j]);
@@ -189,19 +200,18 @@ __global__ void __launch_bounds__(32 * WARPS, BITS8 ? 5 : 4) adamw_multi_kernel(
   k.bc2 *= 0x1p24f;
   const long long b = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
   if (b >= a.blocks) return;
-  int i = 0;  // the tensor of block b
-#pragma unroll 1
-  for (int by = a.search; by > 0; by >>= 1)
-    if (i + by < a.count && a.first[i + by] <= b) i += by;
+  int i = a.hint[b >> a.near_shift];  // the tensor of block b: from that of a block shortly before it
+  while (a.first[i + 1] <= b) ++i;
   const AdamTensor& t = a.t[i];
   const long long e0 = (b - a.first[i]) * BLOCK, e = e0 + lane * 8;
-  const int nb = static_cast<int>(min(static_cast<long long>(BLOCK), t.n - e0));  // elements of this block, > 0
-  const int n = max(0, min(8, nb - lane * 8));
+  const long long left = (t.n2 >> 1) - e0;
+  const bool full = left >= BLOCK;
   const long long at = (a.block0 + b) * BLOCK + lane * 8;  // this lane's place in the states
   P* p = static_cast<P*>(t.p);
   const G* g = static_cast<const G*>(t.g);
   float pv[8], gv[8], m[8], v[8];
-  const bool whole = nb == BLOCK && t.aligned;
+  const bool whole = full && (t.n2 & 1);
+  const int nb = full ? BLOCK : static_cast<int>(left);  // elements of this block, > 0
   uint2 mq, vq;
   float ms, vs;
   if (BITS8) {
@@ -235,10 +245,10 @@ __global__ void __launch_bounds__(32 * WARPS, BITS8 ? 5 : 4) adamw_multi_kernel(
     pv[j] = pv[j] - k.lr * (m[j] * k.bc1 * reciprocal(under) + k.wd * pv[j]);
   }
   if (BITS8) {
-    if (nb < BLOCK) {  // nothing behind the tensor's end
+    if (!full) {  // nothing behind the tensor's end
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j >= n) m[j] = v[j] = 0.f;
+        if (lane * 8 + j >= nb) m[j] = v[j] = 0.f;
     }
     ms = block_top(m);
     vs = block_top(v);
@@ -257,9 +267,10 @@ __global__ void __launch_bounds__(32 * WARPS, BITS8 ? 5 : 4) adamw_multi_kernel(
       }
     }
     // 127 sqrt(m / ms) = sqrt(127^2 m / ms), 255 (v / vs)^(1/4) = sqrt(sqrt(255^4 v / vs))
-    const float mr = ms > 0.f ? 127.f * 127.f / ms : 0.f, vr = vs > 0.f ? 255.f * 255.f * 255.f * 255.f / vs : 0.f;
+    const float mr = ms > 0.f ? 127.f * 127.f * reciprocal(ms) : 0.f;
+    const float vr = vs > 0.f ? 255.f * 255.f * 255.f * 255.f * reciprocal(vs) : 0.f;
     uint32_t mo[8], vo[8];
-    float m_off = 0.f, v_off = 0.f;  // furthest from a whole number
+    float off = 0.f;  // furthest from a whole number
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = copysignf(root(fabsf(m[j]) * mr), m[j]);
@@ -267,12 +278,11 @@ __global__ void __launch_bounds__(32 * WARPS, BITS8 ? 5 : 4) adamw_multi_kernel(
       if (v[j] > 0.f) u = fmaxf(u, 1.f);
       mo[j] = rounded(x);
       vo[j] = rounded(u);
-      m_off = fmaxf(m_off, fabsf(x - rounded_value(mo[j])));
-      v_off = fmaxf(v_off, fabsf(u - rounded_value(vo[j])));
+      asm("max.f32 %0, %1, %2, %3;" : "=f"(off) : "f"(off), "f"(fabsf(x - rounded_value(mo[j]))), "f"(fabsf(u - rounded_value(vo[j]))));
     }
-    // Approximate and correctly rounded values are within 127 (1.5 2^-23 + 2.5 2^-24) = 4.2e-5 of each other
-    // for m, within 255 (1.75 2^-23 + 2.75 2^-24) = 9.5e-5 for v: one warp in 13 has a value that near to a border.
-    if (__any_sync(0xffffffffu, m_off > 0.5f - 5e-5f || v_off > 0.5f - 1e-4f)) {
+    // Approximate and correctly rounded values are within 127 (2 2^-23 + 2.5 2^-24) = 4.9e-5 of each other
+    // for m, within 255 (2 2^-23 + 2.75 2^-24) = 1.03e-4 for v: one warp in ten has a value that near to a border.
+    if (__any_sync(0xffffffffu, off > 0.5f - 1.1e-4f)) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = ms > 0.f ? __fmul_rn(127.f, __fsqrt_rn(__fdiv_rn(fabsf(m[j]), ms))) : 0.f;
@@ -286,13 +296,13 @@ __global__ void __launch_bounds__(32 * WARPS, BITS8 ? 5 : 4) adamw_multi_kernel(
     vq = make_uint2(low_bytes(vo), low_bytes(vo + 4));
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at) = mq;
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at) = vq;
-  } else if (n == 8) {
+  } else if (full || lane * 8 + 8 <= nb) {
     store8(static_cast<float*>(a.m) + at, m);
     store8(static_cast<float*>(a.v) + at, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < n) {
+      if (lane * 8 + j < nb) {
         static_cast<float*>(a.m)[at + j] = m[j];
         static_cast<float*>(a.v)[at + j] = v[j];
       }
@@ -361,13 +371,18 @@ cudaError_t adamw_multi_launch(const soup_adamw_tensor* tensors, int count, cons
       const bool aligned = reinterpret_cast<uintptr_t>(t.p) % (p_bf16 ? 16 : 32) == 0 &&
                            reinterpret_cast<uintptr_t>(t.g) % (g_bf16 ? 16 : 32) == 0 &&
                            reinterpret_cast<uintptr_t>(t.p_bf16_copy) % 16 == 0;
-      a.t[i] = AdamTensor{t.p, t.g, t.p_bf16_copy, t.n, aligned};
+      a.t[i] = AdamTensor{t.p, t.g, t.p_bf16_copy, 2 * t.n + (aligned ? 1 : 0)};
       a.first[i] = a.blocks;
       a.blocks += (t.n + BLOCK - 1) / BLOCK;
     }
     block0 += a.blocks;
     if (a.blocks == 0) continue;
-    for (a.search = 1; 2 * a.search < a.count; a.search *= 2) {
+    a.first[a.count] = a.blocks;
+    for (a.near_shift = 0; ((a.blocks - 1) >> a.near_shift) >= NEAR; ++a.near_shift) {
+    }
+    for (int k = 0, i = 0; (static_cast<long long>(k) << a.near_shift) < a.blocks; ++k) {
+      while (a.first[i + 1] <= (static_cast<long long>(k) << a.near_shift)) ++i;
+      a.hint[k] = static_cast<uint16_t>(i);
     }
     const unsigned grid = static_cast<unsigned>((a.blocks + WARPS - 1) / WARPS);
     if (p_bf16)

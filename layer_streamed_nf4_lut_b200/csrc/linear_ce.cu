@@ -36,7 +36,7 @@ constexpr int TILE = 256;            // rows and columns of a CTA pair's output 
 constexpr int GROUP = TILE / 2;      // columns a group of four epilogue warps works through
 constexpr int BK = 64;               // k-block: 64 bf16 = one 128-byte swizzle row
 constexpr int STAGES = 6;            // operand ring
-constexpr int CHUNK = 16;            // k-blocks of a logit that one accumulator adds up (see ce_gemm_kernel)
+constexpr int CHUNK = 32;            // k-blocks of a logit that one accumulator adds up (see ce_gemm_kernel)
 constexpr int OPERAND = 128 * 128;   // bytes of one operand's k-block in one CTA (128 rows x 64 bf16)
 constexpr int STAGE_BYTES = 2 * OPERAND;
 constexpr int STAGING = 2 * 16384;   // epilogue: a box of 128 rows x 128 bytes for each group of four warps
@@ -161,10 +161,11 @@ __device__ __forceinline__ Unit unit_of(const CeGemm& p, int m_tiles, int splits
 // in tensor memory so that a tile's epilogue runs beside the next tile's products.
 // GRAD = false: logits tile -> P, sums.  GRAD = true: P W -> accumulator of the tile's share.
 //
-// A logit is added up in chunks of 1024 products, by turns in the two accumulators, and the chunks in the
-// epilogue's registers: the tensor cores cut off what falls below an accumulator's last bit, and over
-// 8192 products these cuts, all towards zero, moved a row's lse by 1.9e-5 (1.4e-6 of it), four times
-// what fp32 sums give.  It also frees an accumulator as soon as it is read, before the exponentials.
+// A logit is added up in chunks of 2048 products, by turns in the two accumulators, and the chunks in the
+// epilogue's registers: the tensor cores cut off what falls below an accumulator's last bit, always towards
+// zero, and over 8192 products that moved lse by 1.4e-6 of itself and log-probs by 3.4e-6.  In chunks of
+// 4096 / 2048 / 1024: lse 7e-7 / 3.2e-7 / 1.6e-7 (fp32 sums on the ordinary cores: 8e-7), at 5764 / 5774 / 5816
+// us for 2048 x 8192 x 128256.  An accumulator is also free again as soon as it is read, before the exponentials.
 template <bool GRAD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_kernel(const __grid_constant__ CeGemm p) {
   extern __shared__ uint8_t smem_raw[];
