@@ -52,10 +52,9 @@ constexpr float REF_ROOM = 1.2089258e24f;  // 2^80: how far a tile's sum may lie
 
 struct CeGemm {
   CUtensorMap ta, tb, to;
-  const int* n_rows;  // rows in use (device)
+  const int* n_rows;  // rows in use, and K ranges of the gradient's tiles (device)
   int n_tiles;        // output tiles of 256 columns
   int kb;             // k-blocks
-  int kb_first;       // gradient: k-blocks of the first piece (they fix how tiles are cut)
   int tcap;           // rows of a part_* column
   int cols;           // columns in use
   int accumulate;     // gradient: add to the accumulator instead of writing it
@@ -121,22 +120,27 @@ __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.laun
 // the clock rises under the power limit when fewer work.  Measured, 1 / 2 / 3 ranges: 1108 / 901 / 977 us
 // at 512 x 4096 x 128256 (32 tiles on 74 pairs), 1691 / 1720 / 1734 at 1024, 2700 / 2530 / 2490 at 1500,
 // 6566 / 6430 / 6683 at 2048 x 8192, 1793 / 1842 / 1908 at 4096 x 2048 x 64000.
-__host__ __device__ inline int grad_splits(int m_tiles, int H, int pairs, int kb_first) {
+inline int grad_splits(int m_tiles, int H, int pairs, int kb_first) {
   const int tiles = m_tiles * ((H + TILE - 1) / TILE);
   const long long room = ACC_BYTES / (4ll * TILE * H) / (m_tiles < 1 ? 1 : m_tiles);
   const int most = room < MAX_SPLITS ? static_cast<int>(room) : MAX_SPLITS;
   int best = 1;
-  float cost = 1e30f;
-  for (int s = 1; s <= most && s <= kb_first; ++s) {
-    const float busy = static_cast<float>(tiles * s), wide = 0.93f * ((tiles * s + pairs - 1) / pairs * pairs);
-    const float c = (busy > wide ? busy : wide) * (static_cast<float>(kb_first) / s + 10.f);
-    if (c < cost) {
+  long long cost = 0;  // of best, times best
+  for (int s = 1; s == 1 || (s <= most && s <= kb_first); ++s) {
+    const long long busy = 100ll * tiles * s, wide = 93ll * ((tiles * s + pairs - 1) / pairs * pairs);
+    const long long c = (busy > wide ? busy : wide) * (kb_first + 10 * s);
+    if (s == 1 || c * best < cost * s) {
       cost = c;
       best = s;
     }
   }
   return best;
 }
+
+constexpr int ROW_BLOCK = 4096;  // rows that share one walk over the vocabulary
+struct Splits {                  // for each number of row tiles; how many have rows with targets is known on the device
+  int of[ROW_BLOCK / TILE + 1];
+};
 
 // One output tile, or one K range of it, of a persistent CTA pair's list: row tiles fastest and K ranges
 // slowest, so that the pairs at work read the same k-blocks at about the same time (cutting all tiles'
@@ -208,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
   pdl_wait();
   const int rows = *p.n_rows;
   const int m_tiles = (rows + TILE - 1) / TILE;
-  const int splits = GRAD ? grad_splits(m_tiles, p.cols, pairs, p.kb_first) : 1;
+  const int splits = GRAD ? p.n_rows[1] : 1;
   const int units = m_tiles * p.n_tiles * splits;
 
   // The two issuing warps run their loops whole, with one lane elected for what is issued: descriptors and
@@ -460,7 +464,8 @@ __device__ __forceinline__ int2 targets_of(const int32_t* t1, const int32_t* t2,
 __global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh, const uint16_t* __restrict__ w,
                                   long long ldw, int T, int H, int V, const int32_t* __restrict__ t1,
                                   const int32_t* __restrict__ t2, uint16_t* __restrict__ packed, CeRows rows,
-                                  int* __restrict__ place, int* __restrict__ n_rows, int* __restrict__ raised, int pieces,
+                                  int* __restrict__ place, int* __restrict__ n_rows, const Splits splits,
+                                  int* __restrict__ raised, int pieces,
                                   float* __restrict__ lse, float* __restrict__ logp, float* __restrict__ logp2, int* err) {
   __shared__ float red[32];
   __shared__ int before;
@@ -478,7 +483,11 @@ __global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh,
   __syncthreads();
   const int2 tg = targets_of(t1, t2, t, V, threadIdx.x == 0 ? err : nullptr);
   const int at = before;
-  if (t == T - 1 && threadIdx.x == 0) *n_rows = at + (tg.x >= 0);
+  if (t == T - 1 && threadIdx.x == 0) {
+    const int n_all = at + (tg.x >= 0);
+    n_rows[0] = n_all;
+    n_rows[1] = splits.of[(n_all + TILE - 1) / TILE];
+  }
   if (tg.x < 0) {
     if (threadIdx.x == 0) {
       place[t] = -1;
@@ -524,13 +533,13 @@ __global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh,
 // piece's flag is down.
 __global__ void ce_raise_kernel(const int* __restrict__ raised, const int* __restrict__ n_rows, int tile0, int parts,
                                 int tcap, const float* __restrict__ part_r, float* __restrict__ ref,
-                                uint16_t* __restrict__ P, long long ldp, float* __restrict__ acc, int pairs, int kb_first, int H,
+                                uint16_t* __restrict__ P, long long ldp, float* __restrict__ acc, int H,
                                 int accumulated) {
   pdl_launch();
   pdl_wait();
   if (*raised == 0) return;
   const int rows = *n_rows, m_tiles = (rows + TILE - 1) / TILE;
-  const int splits = grad_splits(m_tiles, H, pairs, kb_first);
+  const int splits = n_rows[1];
   const int lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x >> 5);
   for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows; r += warps) {
     float top = ref[r];
@@ -558,73 +567,82 @@ __global__ void ce_raise_kernel(const int* __restrict__ raised, const int* __res
   }
 }
 
-// Sums of each row's parts (32 rows per block: lane = row, the warps share the parts and their sums
-// are added in warp order), log-probs and lse.  The scalars of a row are formed in 64 bits.
-constexpr int STATS_WARPS = 32;
-__global__ void __launch_bounds__(32 * STATS_WARPS) ce_stats_kernel(const int* __restrict__ n_rows, int parts, int tcap, const float* __restrict__ part_s,
-                                const float* __restrict__ part_r, CeRows rows, float* __restrict__ out_lse,
-                                float* __restrict__ out_logp, float* __restrict__ out_logp2) {
-  __shared__ float sums[STATS_WARPS][32], refs[STATS_WARPS][32];
+// Sums of each row's parts, log-probs and lse.  A block takes 8 rows (a 32-byte sector of each part), 32
+// threads the parts of a row; then a warp takes a row, adds the threads' sums in a fixed order in 64 bits
+// and forms the row's scalars in 64 bits, the logarithms side by side in three lanes.
+constexpr int STATS_ROWS = 8;
+__global__ void __launch_bounds__(32 * STATS_ROWS) ce_stats_kernel(const int* __restrict__ n_rows, int parts, int tcap,
+                                                                   const float* __restrict__ part_s,
+                                                                   const float* __restrict__ part_r, CeRows rows,
+                                                                   float* __restrict__ out_lse, float* __restrict__ out_logp,
+                                                                   float* __restrict__ out_logp2) {
+  __shared__ float sums[32][STATS_ROWS], refs[32][STATS_ROWS];
   pdl_launch();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = blockIdx.x * 32 + lane;
-  const bool live = r < *n_rows;
-  float top = -INFINITY, sum = 0.f;
-  if (live) {
-    top = rows.ref[r];
-    // eight parts at a time, so that their loads are in flight together
-    for (int i = warp; i < parts; i += 8 * STATS_WARPS) {
-      float s[8], k[8];
+  const int n = *n_rows, r0 = blockIdx.x * STATS_ROWS;
+  if (r0 >= n) return;
+  {
+    const int row = threadIdx.x % STATS_ROWS, first = threadIdx.x / STATS_ROWS, r = r0 + row;  // r < tcap
+    float top = -INFINITY, sum = 0.f;
+    if (r < n) {
+      top = rows.ref[r];
+      // eight parts at a time, so that their loads are in flight together
+      for (int i = first; i < parts; i += 8 * 32) {
+        float s[8], k[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int q = i + j * STATS_WARPS;
-        const long long at = static_cast<long long>(q) * tcap + r;
-        s[j] = q < parts ? part_s[at] : 0.f;
-        k[j] = q < parts ? part_r[at] : top;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (k[j] > top) {
-          sum *= exp2f(top - k[j]);
-          top = k[j];
+        for (int j = 0; j < 8; ++j) {
+          const int q = i + j * 32;
+          const long long at = static_cast<long long>(q) * tcap + r;
+          s[j] = q < parts ? part_s[at] : 0.f;
+          k[j] = q < parts ? part_r[at] : top;
         }
-        sum += k[j] == top ? s[j] : s[j] * exp2f(k[j] - top);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (k[j] > top) {
+            sum *= exp2f(top - k[j]);
+            top = k[j];
+          }
+          sum += k[j] == top ? s[j] : s[j] * exp2f(k[j] - top);
+        }
       }
     }
+    sums[first][row] = sum;
+    refs[first][row] = top;
   }
-  sums[warp][lane] = sum;
-  refs[warp][lane] = top;
   __syncthreads();
-  if (warp != 0 || !live) return;
-  for (int i = 1; i < STATS_WARPS; ++i) top = fmaxf(top, refs[i][lane]);
-  double other = 0.0;
-  for (int i = 0; i < STATS_WARPS; ++i)
-    other += static_cast<double>(sums[i][lane]) *
-             (refs[i][lane] == top ? 1.0 : exp2(static_cast<double>(refs[i][lane] - top)));
+  const int row = threadIdx.x >> 5, lane = threadIdx.x & 31, r = r0 + row;
+  if (r >= n) return;
+  const float top = warp_max(refs[lane][row]);
+  double other = static_cast<double>(sums[lane][row]);
+  if (refs[lane][row] != top) other *= exp2(static_cast<double>(refs[lane][row] - top));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) other += __shfl_xor_sync(0xffffffffu, other, o);
   const int2 tg = rows.target[r];
   const bool two = tg.y >= 0 && tg.y != tg.x;
   const double ln2 = 0.6931471805599453;
-  const double a = static_cast<double>(rows.la[r]) - top, b = static_cast<double>(rows.lb[r]) - top;
-  const double ea = exp2(a), eb = two ? exp2(b) : 0.0;
-  const double z = other + ea + eb, lz = log(z);
-  const double rest_a = other + eb, rest_b = other + ea;
-  const double lpa = ea > rest_a ? -log1p(rest_a / ea) : a * ln2 - lz;
-  const double lpb = two ? (eb > rest_b ? -log1p(rest_b / eb) : b * ln2 - lz) : lpa;
-  rows.inv_z[r] = static_cast<float>(1.0 / z);
-  rows.pa[r] = make_float2(static_cast<float>(ea / z), static_cast<float>(rest_a / z));
-  rows.pb[r] = make_float2(static_cast<float>(eb / z), static_cast<float>(rest_b / z));
+  // lane 1: the second target, the others the first
+  const double mine = static_cast<double>(lane == 1 ? rows.lb[r] : rows.la[r]) - top;
+  const double e = lane == 1 && !two ? 0.0 : exp2(mine);
+  const double ea = __shfl_sync(0xffffffffu, e, 0), eb = __shfl_sync(0xffffffffu, e, 1);
+  const double z = other + ea + eb, rest = other + (lane == 1 ? ea : eb);  // of the lane's own target
+  // lane 2: log z (z is at least about 0.7: the largest term's ref is its own exponent)
+  const double l = log1p(lane == 2 ? z - 1.0 : rest / e);
+  const double lz = __shfl_sync(0xffffffffu, l, 2);
+  const double lp = e > rest ? -l : mine * ln2 - lz;
+  const double lpa = __shfl_sync(0xffffffffu, lp, 0), lpb = __shfl_sync(0xffffffffu, lp, 1);
   const int t = rows.row[r];
-  if (out_lse) out_lse[t] = static_cast<float>(static_cast<double>(top) * ln2 + lz);
-  out_logp[t] = static_cast<float>(lpa);
-  if (out_logp2) out_logp2[t] = tg.y >= 0 ? static_cast<float>(lpb) : 0.f;
+  if (lane < 2) (lane ? rows.pb : rows.pa)[r] = make_float2(static_cast<float>(e / z), static_cast<float>(rest / z));
+  if (lane == 2) rows.inv_z[r] = static_cast<float>(1.0 / z);
+  if (lane == 3 && out_lse) out_lse[t] = static_cast<float>(static_cast<double>(top) * ln2 + lz);
+  if (lane == 4) out_logp[t] = static_cast<float>(lpa);
+  if (lane == 5 && out_logp2) out_logp2[t] = tg.y >= 0 ? static_cast<float>(two ? lpb : lpa) : 0.f;
 }
 
 // dh of one row of the batch per block: the accumulators of the tile's shares, added in order, and the
 // targets' rows of W with coefficients formed from 1 - p.
 __global__ void ce_dh_kernel(const int* __restrict__ place, CeRows rows, const float* __restrict__ weight,
                              const float* __restrict__ weight2, const float* __restrict__ acc,
-                             const int* __restrict__ n_rows, int pairs, int kb_first,
+                             const int* __restrict__ n_rows,
                              const uint16_t* __restrict__ w, long long ldw, int H, uint16_t* __restrict__ dh,
                              long long ldd) {
   pdl_launch();
@@ -651,7 +669,7 @@ __global__ void ce_dh_kernel(const int* __restrict__ place, CeRows rows, const f
   const uint16_t* wa = w + tg.x * ldw;
   const uint16_t* wb = w + (two ? tg.y : tg.x) * ldw;
   const int m_tiles = (*n_rows + TILE - 1) / TILE, m = r / TILE;
-  const int splits = grad_splits(m_tiles, H, pairs, kb_first);
+  const int splits = n_rows[1];
   for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
     float v[8];
 #pragma unroll
@@ -678,7 +696,6 @@ __global__ void ce_dh_kernel(const int* __restrict__ place, CeRows rows, const f
 }
 
 // ---------------------------------------------------------------- the plan
-constexpr int ROW_BLOCK = 4096;           // rows that share one walk over the vocabulary
 constexpr long long P_BYTES = 96ll << 20; // of one piece's P: half of the L2
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -686,6 +703,7 @@ size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 struct CePlan {
   int pairs, block, blocks, tcap, tiles, piece_tiles, pieces, h_tiles, kb_first;
   long long acc_rows;
+  Splits splits;
   // byte offsets: per row block (stride per_block), then shared by the blocks
   size_t n_rows, place, target, row, ref, la, lb, inv_z, pa, pb, acc, per_block;
   size_t raised, packed, part_s, part_r, p, total;
@@ -709,8 +727,10 @@ CePlan ce_plan(int T, int H, int V, bool grad, int sms) {
     if (waves >= 1 && n < q.tiles) n = waves * q.pairs / mt;
     q.piece_tiles = static_cast<int>(std::max(1ll, n));
     q.kb_first = (std::min(V, q.piece_tiles * TILE) + BK - 1) / BK;
-    for (int m = 1; m <= mt; ++m)  // whatever the number of rows with targets turns out to be
-      q.acc_rows = std::max(q.acc_rows, static_cast<long long>(TILE) * m * grad_splits(m, H, q.pairs, q.kb_first));
+    for (int m = 0; m <= mt; ++m) {
+      q.splits.of[m] = grad_splits(m, H, q.pairs, q.kb_first);
+      q.acc_rows = std::max(q.acc_rows, static_cast<long long>(TILE) * m * q.splits.of[m]);
+    }
   }
   q.pieces = (q.tiles + q.piece_tiles - 1) / q.piece_tiles;
   size_t o = 0;
@@ -720,7 +740,7 @@ CePlan ce_plan(int T, int H, int V, bool grad, int sms) {
     o += up256(bytes);
     return at;
   };
-  q.n_rows = take(4);
+  q.n_rows = take(8);
   q.place = take(rows * 4);
   q.target = take(rows * 8);
   q.row = take(rows * 4);
@@ -817,7 +837,6 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
   a.store_p = grad;
   a.err = b.err = err;
   b.n_tiles = q.h_tiles;
-  b.kb_first = q.kb_first;
   b.cols = H;
   for (int k = 0; k < q.blocks; ++k) {
     const int t0 = k * q.block, n = std::min(q.block, T - t0), mt = (n + TILE - 1) / TILE;
@@ -826,7 +845,8 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
     int* n_rows = reinterpret_cast<int*>(base + q.n_rows);
     float* acc = reinterpret_cast<float*>(base + q.acc);
     CE_CK(launch(ce_prepare_kernel, n, row_threads(H), 0, st, h + t0 * ldh, ldh, w, ldw, n, H, V, t1 + t0,
-                 t2 ? t2 + t0 : nullptr, packed, rows, reinterpret_cast<int*>(base + q.place), n_rows, raised, q.pieces,
+                 t2 ? t2 + t0 : nullptr, packed, rows, reinterpret_cast<int*>(base + q.place), n_rows, q.splits, raised,
+                 q.pieces,
                  lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr, err));
     if (grad && !tma_encode_sw128(&b.to, acc, true, H, static_cast<unsigned long long>(q.acc_rows), 4ull * H, 32, 128))
       return cudaErrorInvalidValue;
@@ -843,12 +863,12 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
       CE_CK(launch(ce_gemm_kernel<false>, 2 * std::min(q.pairs, mt * a.n_tiles), THREADS, SMEM_BYTES, st, a));
       if (!grad) continue;
       CE_CK(launch(ce_raise_kernel, 64, 256, 0, st, raised + i, n_rows, a.tile0, a.n_tiles, q.tcap, part_r,
-                   rows.ref, P, ldp, acc, q.pairs, q.kb_first, H, i > 0));
+                   rows.ref, P, ldp, acc, H, i > 0));
       b.kb = (a.cols + BK - 1) / BK;
       b.accumulate = i > 0;
       CE_CK(launch(ce_gemm_kernel<true>, 2 * q.pairs, THREADS, SMEM_BYTES, st, b));
     }
-    CE_CK(launch(ce_stats_kernel, (n + 31) / 32, 32 * STATS_WARPS, 0, st, n_rows, q.tiles, q.tcap, part_s, part_r, rows,
+    CE_CK(launch(ce_stats_kernel, (n + STATS_ROWS - 1) / STATS_ROWS, 32 * STATS_ROWS, 0, st, n_rows, q.tiles, q.tcap, part_s, part_r, rows,
                  lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr));
   }
   return cudaSuccess;
@@ -862,7 +882,7 @@ cudaError_t linear_ce_bwd_launch(const uint16_t* w, long long ldw, int T, int H,
     uint8_t* base = ws + k * q.per_block;
     CE_CK(launch(ce_dh_kernel, n, row_threads(H), 0, st, reinterpret_cast<int*>(base + q.place), rows_of(q, base),
                  weight + t0, weight2 ? weight2 + t0 : nullptr, reinterpret_cast<float*>(base + q.acc),
-                 reinterpret_cast<int*>(base + q.n_rows), q.pairs, q.kb_first, w, ldw, H, dh + t0 * ldd, ldd));
+                 reinterpret_cast<int*>(base + q.n_rows), w, ldw, H, dh + t0 * ldd, ldd));
   }
   return cudaSuccess;
 }
