@@ -43,12 +43,28 @@ constexpr int STAGING = 2 * 16384;   // epilogue: a box of 128 rows x 128 bytes 
 constexpr int BARRIERS = 256;
 constexpr int JOIN = 2 * 128 * 4;    // epilogue: the second group's sums, for the first one
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING + BARRIERS + JOIN + 1024;
-constexpr int THREADS = 384;         // warp 0 TMA, 1 MMA, 2 TMEM, 3 idle, 4-11 epilogue
-constexpr int MAX_SPLITS = 16;
+constexpr int THREADS = 384;         // warp 0 TMA, 1 MMA, 2 TMEM, 3 log-probs, 4-11 epilogue
+constexpr int MAX_SPLITS = 80;
 constexpr long long ACC_BYTES = 144ll << 20; // of all accumulators, unless one for each tile takes more
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float REF_ROOM = 1.2089258e24f;  // 2^80: how far a tile's sum may lie above its ref; what is made of it
                                            // (2^17 terms, products with W) stays below fp32's 2^128
+
+struct CeRows {  // per packed row
+  int2* target;
+  int* row;              // its row in the batch
+  float *ref, *la, *lb;  // ref and the targets' logits, in powers of two
+  float* inv_z;          // once the vocabulary is done: 1 / Z against ref,
+  float2 *pa, *pb;       // and each target's p and 1 - p
+};
+
+// What the log-probs of all rows are formed from, and where they go.
+struct CeStats {
+  int parts, tcap;
+  const float *part_s, *part_r;
+  CeRows rows;
+  float *lse, *logp, *logp2;
+};
 
 struct CeGemm {
   CUtensorMap ta, tb, to;
@@ -64,7 +80,14 @@ struct CeGemm {
   float *part_s, *part_r;  // [tile of the vocabulary][tcap]: their sum and the ref it is against
   int tile0;          // first vocabulary tile of this piece
   int store_p;
-  int* raised;
+  int* raised;        // [0]: a row's ref was raised in this piece, [1]: CTAs done with it
+  uint16_t* P;        // where `to` stores, for the rows whose ref was raised,
+  long long ldp;
+  float* acc;         // and the gradient's accumulators, if earlier pieces are in them
+  float* row_ref;
+  int acc_cols;
+  int with_stats;     // gradient: the last piece's, which also forms the log-probs
+  CeStats stats;
   int* err;
 };
 
@@ -73,6 +96,8 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Orders what the async proxy (TMA) and ordinary accesses do to global memory.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ bool elect_one() {
   uint32_t is;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
@@ -159,6 +184,90 @@ __device__ __forceinline__ Unit unit_of(const CeGemm& p, int m_tiles, int splits
   t.kb_lo = GRAD ? static_cast<int>(static_cast<long long>(p.kb) * t.share / splits) : 0;
   t.kb_hi = GRAD ? static_cast<int>(static_cast<long long>(p.kb) * (t.share + 1) / splits) : p.kb;
   return t;
+}
+
+// Rows that met a logit beyond their ref's room: P of this piece and the accumulators go to the
+// largest ref a part took.  Powers of two: exact.  By the piece's last CTA, a warp a row; rare (a target
+// 2^80 times less likely than another token), so one CTA is enough.
+__device__ __noinline__ void raise_rows(const CeGemm& p, int rows, int m_tiles, int splits) {
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < rows; r += THREADS / 32) {
+    const float before = __ldcg(p.row_ref + r);
+    float top = before;
+    for (int i = lane; i < p.n_tiles; i += 32) top = fmaxf(top, __ldcg(p.part_r + static_cast<long long>(p.tile0 + i) * p.tcap + r));
+    top = warp_max(top);
+    if (!(top > before)) continue;
+    for (int i = 0; i < p.n_tiles; ++i) {
+      const float have = __ldcg(p.part_r + static_cast<long long>(p.tile0 + i) * p.tcap + r);
+      if (have == top) continue;
+      const float f = exp2f(have - top);
+      uint16_t* q = p.P + r * p.ldp + i * TILE;
+      for (int c = lane; c < TILE; c += 32) {
+        const __nv_bfloat16 v = __float2bfloat16_rn(bf16_to_f32(__ldcg(q + c)) * f);
+        q[c] = *reinterpret_cast<const uint16_t*>(&v);
+      }
+    }
+    if (p.acc) {
+      const float f = exp2f(before - top);
+      const int m = r / TILE;
+      for (int c = lane; c < p.acc_cols; c += 32)
+        for (int j = 0; j < splits; ++j)
+          p.acc[(static_cast<long long>(j * m_tiles + m) * TILE + r % TILE) * p.acc_cols + c] *= f;
+    }
+    __syncwarp();
+    if (lane == 0) p.row_ref[r] = top;
+  }
+}
+
+// One row's sums of parts, log-probs and lse, by a warp: parts are added a lane each in a fixed order, the
+// lanes and the row's scalars in 64 bits, the logarithms side by side in three lanes.
+__device__ __noinline__ void row_stats(const CeStats& q, int r) {
+  const int lane = threadIdx.x & 31;
+  float top = q.rows.ref[r], sum = 0.f;
+  // eight parts at a time, so that their loads are in flight together
+  for (int i = lane; i < q.parts; i += 8 * 32) {
+    float s[8], k[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int part = i + j * 32;
+      const long long at = static_cast<long long>(part) * q.tcap + r;
+      s[j] = part < q.parts ? q.part_s[at] : 0.f;
+      k[j] = part < q.parts ? q.part_r[at] : top;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (k[j] > top) {
+        sum *= exp2f(top - k[j]);
+        top = k[j];
+      }
+      sum += k[j] == top ? s[j] : s[j] * exp2f(k[j] - top);
+    }
+  }
+  const float own = top;
+  top = warp_max(top);
+  double other = static_cast<double>(sum);
+  if (own != top) other *= exp2(static_cast<double>(own - top));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) other += __shfl_xor_sync(0xffffffffu, other, o);
+  const int2 tg = q.rows.target[r];
+  const bool two = tg.y >= 0 && tg.y != tg.x;
+  const double ln2 = 0.6931471805599453;
+  // lane 1: the second target, the others the first
+  const double mine = static_cast<double>(lane == 1 ? q.rows.lb[r] : q.rows.la[r]) - top;
+  const double e = lane == 1 && !two ? 0.0 : exp2(mine);
+  const double ea = __shfl_sync(0xffffffffu, e, 0), eb = __shfl_sync(0xffffffffu, e, 1);
+  const double z = other + ea + eb, rest = other + (lane == 1 ? ea : eb);  // of the lane's own target
+  // lane 2: log z (z is at least about 0.5: the largest term lies within a power of two of its ref)
+  const double l = log1p(lane == 2 ? z - 1.0 : rest / e);
+  const double lz = __shfl_sync(0xffffffffu, l, 2);
+  const double lp = e > rest ? -l : mine * ln2 - lz;
+  const double lpa = __shfl_sync(0xffffffffu, lp, 0), lpb = __shfl_sync(0xffffffffu, lp, 1);
+  const int t = q.rows.row[r];
+  if (lane < 2) (lane ? q.rows.pb : q.rows.pa)[r] = make_float2(static_cast<float>(e / z), static_cast<float>(rest / z));
+  if (lane == 2) q.rows.inv_z[r] = static_cast<float>(1.0 / z);
+  if (lane == 3 && q.lse) q.lse[t] = static_cast<float>(static_cast<double>(top) * ln2 + lz);
+  if (lane == 4) q.logp[t] = static_cast<float>(lpa);
+  if (lane == 5 && q.logp2) q.logp2[t] = tg.y >= 0 ? static_cast<float>(two ? lpb : lpa) : 0.f;
 }
 
 // 256 x 256 tiles, one CTA pair each (tcgen05 cta_group::2, M = 256, N = 256), two accumulators
@@ -286,6 +395,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
         if (b == 0) b_phase ^= 1;
       }
     }
+  } else if (GRAD && warp == 3) {
+    // ---- the log-probs, beside the last piece's products
+    if (p.with_stats)
+      for (int r = blockIdx.x; r < rows; r += gridDim.x) row_stats(p.stats, r);
   } else if (warp >= 4) {
     // ---- epilogue: thread = accumulator row; two groups of four warps take half of the columns each
     const int group = (warp - 4) >> 2;
@@ -331,37 +444,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
         if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
         ++n_done;
       } else {
-        float l[GROUP];  // this thread's logits
+        const int r = m0 + row;
+        const bool live = r < rows;
+        const int2 tg = live ? p.target[r] : make_int2(-1, -1);
+        float ref = live ? p.ref[r] : 0.f, total = 0.f;
+        uint32_t l[GROUP];  // this thread's logits
         for (int kb = 0; kb < p.kb; kb += CHUNK) {
           const int buf = n_done & 1;
           if (!epilogue_all(mbar_wait_bounded(&acc_full[buf], (n_done >> 1) & 1, abort_flag, p.err))) goto done;
           tc_fence_after();
           const uint32_t acc = tmem + lanes + buf * TILE + group * GROUP;
+          if (kb == 0) {
 #pragma unroll
-          for (int c = 0; c < GROUP; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(acc + c, v);
+            for (int c = 0; c < GROUP; c += 32) tmem_ld32(acc + c, l + c);
             tmem_ld_wait();
+          } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) l[c + j] = (kb ? l[c + j] : 0.f) + __uint_as_float(v[j]);
+            for (int c = 0; c < GROUP; c += 32) {
+              uint32_t v[32];
+              tmem_ld32(acc + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) l[c + j] = __float_as_uint(__uint_as_float(l[c + j]) + __uint_as_float(v[j]));
+            }
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[buf], 0));
           ++n_done;
         }
-        const int r = m0 + row;
-        const bool live = r < rows;
-        const int2 tg = live ? p.target[r] : make_int2(-1, -1);
         const int ta = tg.x - p.w_row0 - n0, tb = tg.y - p.w_row0 - n0;  // the targets' columns here
         const int valid = p.cols - n0;                                    // columns inside the vocabulary
         // columns that stay out: the targets', for the few rows that have one here, and those past the end
         if (__any_sync(0xffffffffu, (ta >= 0 && ta < GROUP) || (tb >= 0 && tb < GROUP)) || valid < GROUP) {
 #pragma unroll
           for (int j = 0; j < GROUP; ++j)
-            if (j == ta || j == tb || j >= valid) l[j] = -INFINITY;
+            if (j == ta || j == tb || j >= valid) l[j] = 0xff800000u;  // -inf
         }
-        float ref = live ? p.ref[r] : 0.f, total = 0.f;
         for (int attempt = 0; attempt < 2; ++attempt) {
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -369,8 +488,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
             uint32_t w[32];
 #pragma unroll
             for (int j = 0; j < 64; j += 2) {
-              const float e0 = exp2_approx(fmaf(l[c + j], LOG2E, -ref));
-              const float e1 = exp2_approx(fmaf(l[c + j + 1], LOG2E, -ref));
+              const float e0 = exp2_approx(fmaf(__uint_as_float(l[c + j]), LOG2E, -ref));
+              const float e1 = exp2_approx(fmaf(__uint_as_float(l[c + j + 1]), LOG2E, -ref));
               sum[j & 3] += e0;
               sum[(j + 1) & 3] += e1;
               w[j >> 1] = pack_bf16x2(e0, e1);
@@ -401,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
           }
           float top = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < GROUP; ++j) top = fmaxf(top, l[j]);
+          for (int j = 0; j < GROUP; ++j) top = fmaxf(top, __uint_as_float(l[j]));
           if (elected) tma_store_wait_all();  // the boxes are written again, here and below: in order
           group_sync(group);
           *reinterpret_cast<float2*>(my_row) = make_float2(top, over ? 1.f : 0.f);
@@ -421,7 +540,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
         }
       }
     }
-    if (elected) tma_store_wait_all();
+    if (elected) {
+      tma_store_wait_all();
+      if (!GRAD) fence_proxy_async_all();  // P may be read and written again below
+    }
   }
 done:
   __syncwarp();
@@ -437,17 +559,23 @@ done:
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
+  if (!GRAD && p.store_p) {
+    volatile int* is_last = abort_flag + 1;
+    if (threadIdx.x == 0) {
+      __threadfence();
+      *is_last = atomicAdd(p.raised + 1, 1) == static_cast<int>(gridDim.x) - 1;
+      __threadfence();
+    }
+    __syncthreads();
+    if (*is_last && __ldcg(p.raised)) {
+      fence_proxy_async_all();
+      raise_rows(p, rows, m_tiles, p.n_rows[1]);
+      fence_proxy_async_all();
+    }
+  }
 }
 
 // ---------------------------------------------------------------- rows
-struct CeRows {  // per packed row
-  int2* target;
-  int* row;              // its row in the batch
-  float *ref, *la, *lb;  // ref and the targets' logits, in powers of two
-  float* inv_z;          // once the vocabulary is done: 1 / Z against ref,
-  float2 *pa, *pb;       // and each target's p and 1 - p
-};
-
 __device__ __forceinline__ int2 targets_of(const int32_t* t1, const int32_t* t2, int t, int V, int* err) {
   int a = t1[t], b = t2 ? t2[t] : -1;
   if (a >= V || b >= V) {
@@ -463,7 +591,8 @@ __device__ __forceinline__ int2 targets_of(const int32_t* t1, const int32_t* t2,
 // targets' logits in fp32.
 __global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh, const uint16_t* __restrict__ w,
                                   long long ldw, int T, int H, int V, const int32_t* __restrict__ t1,
-                                  const int32_t* __restrict__ t2, uint16_t* __restrict__ packed, CeRows rows,
+                                  const int32_t* __restrict__ t2, uint16_t* __restrict__ packed, long long ldp,
+                                  CeRows rows,
                                   int* __restrict__ place, int* __restrict__ n_rows, const Splits splits,
                                   int* __restrict__ raised, int pieces,
                                   float* __restrict__ lse, float* __restrict__ logp, float* __restrict__ logp2, int* err) {
@@ -479,7 +608,7 @@ __global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh,
   n = __reduce_add_sync(0xffffffffu, n);
   if ((threadIdx.x & 31) == 0 && n) atomicAdd(&before, n);
   if (t == 0)
-    for (int i = threadIdx.x; i < pieces; i += blockDim.x) raised[i] = 0;
+    for (int i = threadIdx.x; i < 2 * pieces; i += blockDim.x) raised[i] = 0;
   __syncthreads();
   const int2 tg = targets_of(t1, t2, t, V, threadIdx.x == 0 ? err : nullptr);
   const int at = before;
@@ -505,7 +634,7 @@ __global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh,
     const uint4 hv = *reinterpret_cast<const uint4*>(hr + c);
     const uint4 av = *reinterpret_cast<const uint4*>(wa + c);
     const uint4 bv = *reinterpret_cast<const uint4*>(wb + c);
-    *reinterpret_cast<uint4*>(packed + static_cast<long long>(at) * H + c) = hv;
+    *reinterpret_cast<uint4*>(packed + static_cast<long long>(at) * ldp + c) = hv;
     const uint32_t hw[4] = {hv.x, hv.y, hv.z, hv.w}, aw[4] = {av.x, av.y, av.z, av.w}, bw[4] = {bv.x, bv.y, bv.z, bv.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -528,114 +657,12 @@ __global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh,
   }
 }
 
-// Rows that met a logit beyond their ref's room: P of this piece and the accumulators go to the
-// largest ref a part took.  Powers of two: exact.  One warp per row; nothing to do while the
-// piece's flag is down.
-__global__ void ce_raise_kernel(const int* __restrict__ raised, const int* __restrict__ n_rows, int tile0, int parts,
-                                int tcap, const float* __restrict__ part_r, float* __restrict__ ref,
-                                uint16_t* __restrict__ P, long long ldp, float* __restrict__ acc, int H,
-                                int accumulated) {
+// The log-probs of all rows, where no gradient's kernel forms them: a warp a row.
+__global__ void __launch_bounds__(128) ce_stats_kernel(const int* __restrict__ n_rows, const CeStats q) {
   pdl_launch();
   pdl_wait();
-  if (*raised == 0) return;
-  const int rows = *n_rows, m_tiles = (rows + TILE - 1) / TILE;
-  const int splits = n_rows[1];
-  const int lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x >> 5);
-  for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows; r += warps) {
-    float top = ref[r];
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, part_r[static_cast<long long>(tile0 + i) * tcap + r]);
-    top = warp_max(top);
-    if (!(top > ref[r])) continue;
-    for (int i = 0; i < parts; ++i) {
-      const float have = part_r[static_cast<long long>(tile0 + i) * tcap + r];
-      if (have == top) continue;
-      const float f = exp2f(have - top);
-      uint16_t* q = P + r * ldp + i * TILE;
-      for (int c = lane; c < TILE; c += 32) {
-        const __nv_bfloat16 v = __float2bfloat16_rn(bf16_to_f32(q[c]) * f);
-        q[c] = *reinterpret_cast<const uint16_t*>(&v);
-      }
-    }
-    if (accumulated) {
-      const float f = exp2f(ref[r] - top);
-      const int m = r / TILE;
-      for (int c = lane; c < H; c += 32)
-        for (int j = 0; j < splits; ++j) acc[(static_cast<long long>(j * m_tiles + m) * TILE + r % TILE) * H + c] *= f;
-    }
-    __syncwarp();
-    if (lane == 0) ref[r] = top;
-  }
-}
-
-// Sums of each row's parts, log-probs and lse.  A block takes 8 rows (a 32-byte sector of each part), 32
-// threads the parts of a row; then a warp takes a row, adds the threads' sums in a fixed order in 64 bits
-// and forms the row's scalars in 64 bits, the logarithms side by side in three lanes.
-constexpr int STATS_ROWS = 8;
-__global__ void __launch_bounds__(32 * STATS_ROWS) ce_stats_kernel(const int* __restrict__ n_rows, int parts, int tcap,
-                                                                   const float* __restrict__ part_s,
-                                                                   const float* __restrict__ part_r, CeRows rows,
-                                                                   float* __restrict__ out_lse, float* __restrict__ out_logp,
-                                                                   float* __restrict__ out_logp2) {
-  __shared__ float sums[32][STATS_ROWS], refs[32][STATS_ROWS];
-  pdl_launch();
-  pdl_wait();
-  const int n = *n_rows, r0 = blockIdx.x * STATS_ROWS;
-  if (r0 >= n) return;
-  {
-    const int row = threadIdx.x % STATS_ROWS, first = threadIdx.x / STATS_ROWS, r = r0 + row;  // r < tcap
-    float top = -INFINITY, sum = 0.f;
-    if (r < n) {
-      top = rows.ref[r];
-      // eight parts at a time, so that their loads are in flight together
-      for (int i = first; i < parts; i += 8 * 32) {
-        float s[8], k[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int q = i + j * 32;
-          const long long at = static_cast<long long>(q) * tcap + r;
-          s[j] = q < parts ? part_s[at] : 0.f;
-          k[j] = q < parts ? part_r[at] : top;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (k[j] > top) {
-            sum *= exp2f(top - k[j]);
-            top = k[j];
-          }
-          sum += k[j] == top ? s[j] : s[j] * exp2f(k[j] - top);
-        }
-      }
-    }
-    sums[first][row] = sum;
-    refs[first][row] = top;
-  }
-  __syncthreads();
-  const int row = threadIdx.x >> 5, lane = threadIdx.x & 31, r = r0 + row;
-  if (r >= n) return;
-  const float top = warp_max(refs[lane][row]);
-  double other = static_cast<double>(sums[lane][row]);
-  if (refs[lane][row] != top) other *= exp2(static_cast<double>(refs[lane][row] - top));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) other += __shfl_xor_sync(0xffffffffu, other, o);
-  const int2 tg = rows.target[r];
-  const bool two = tg.y >= 0 && tg.y != tg.x;
-  const double ln2 = 0.6931471805599453;
-  // lane 1: the second target, the others the first
-  const double mine = static_cast<double>(lane == 1 ? rows.lb[r] : rows.la[r]) - top;
-  const double e = lane == 1 && !two ? 0.0 : exp2(mine);
-  const double ea = __shfl_sync(0xffffffffu, e, 0), eb = __shfl_sync(0xffffffffu, e, 1);
-  const double z = other + ea + eb, rest = other + (lane == 1 ? ea : eb);  // of the lane's own target
-  // lane 2: log z (z is at least about 0.7: the largest term's ref is its own exponent)
-  const double l = log1p(lane == 2 ? z - 1.0 : rest / e);
-  const double lz = __shfl_sync(0xffffffffu, l, 2);
-  const double lp = e > rest ? -l : mine * ln2 - lz;
-  const double lpa = __shfl_sync(0xffffffffu, lp, 0), lpb = __shfl_sync(0xffffffffu, lp, 1);
-  const int t = rows.row[r];
-  if (lane < 2) (lane ? rows.pb : rows.pa)[r] = make_float2(static_cast<float>(e / z), static_cast<float>(rest / z));
-  if (lane == 2) rows.inv_z[r] = static_cast<float>(1.0 / z);
-  if (lane == 3 && out_lse) out_lse[t] = static_cast<float>(static_cast<double>(top) * ln2 + lz);
-  if (lane == 4) out_logp[t] = static_cast<float>(lpa);
-  if (lane == 5 && out_logp2) out_logp2[t] = tg.y >= 0 ? static_cast<float>(two ? lpb : lpa) : 0.f;
+  const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (r < *n_rows) row_stats(q, r);
 }
 
 // dh of one row of the batch per block: the accumulators of the tile's shares, added in order, and the
@@ -670,17 +697,39 @@ __global__ void ce_dh_kernel(const int* __restrict__ place, CeRows rows, const f
   const uint16_t* wb = w + (two ? tg.y : tg.x) * ldw;
   const int m_tiles = (*n_rows + TILE - 1) / TILE, m = r / TILE;
   const int splits = n_rows[1];
-  for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
+  // Threads take 8 columns each; where that leaves threads over, groups of them share the accumulators, and
+  // their sums are added in order.
+  const int cols = H / 8, per = min(cols, static_cast<int>(blockDim.x)), groups = blockDim.x / per, g = threadIdx.x / per;
+  extern __shared__ float4 sums[];  // [groups][2 per]
+  for (int c0 = 0; c0 < cols; c0 += per) {
+    const int c8 = c0 + threadIdx.x % per, c = 8 * c8;
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
-    for (int s = 0; s < splits; ++s) {
-      const float4* q = reinterpret_cast<const float4*>(
-          acc + (static_cast<long long>(s * m_tiles + m) * TILE + r % TILE) * H + c);
-      const float4 x = q[0], y = q[1];
-      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    if (c8 < cols && g < groups) {
+      const float* q = acc + (static_cast<long long>(m) * TILE + r % TILE) * H + c;
+      const long long next = static_cast<long long>(m_tiles) * TILE * H;
+#pragma unroll 4
+      for (int s = g; s < splits; s += groups) {
+        const float4 x = *reinterpret_cast<const float4*>(q + s * next), y = *reinterpret_cast<const float4*>(q + s * next + 4);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
     }
+    if (groups > 1) {  // then there is one round
+      if (g < groups) {
+        sums[2 * (g * per + c8)] = make_float4(v[0], v[1], v[2], v[3]);
+        sums[2 * (g * per + c8) + 1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+      __syncthreads();
+      if (g > 0) return;
+      for (int i = 1; i < groups; ++i) {
+        const float4 x = sums[2 * (i * per + c8)], y = sums[2 * (i * per + c8) + 1];
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
+    }
+    if (c8 >= cols || g > 0) continue;
     const uint4 av = *reinterpret_cast<const uint4*>(wa + c);
     const uint4 bv = *reinterpret_cast<const uint4*>(wb + c);
     const uint32_t aw[4] = {av.x, av.y, av.z, av.w}, bw[4] = {bv.x, bv.y, bv.z, bv.w};
@@ -702,7 +751,7 @@ size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct CePlan {
   int pairs, block, blocks, tcap, tiles, piece_tiles, pieces, h_tiles, kb_first;
-  long long acc_rows;
+  long long acc_rows, ld_packed;
   Splits splits;
   // byte offsets: per row block (stride per_block), then shared by the blocks
   size_t n_rows, place, target, row, ref, la, lb, inv_z, pa, pb, acc, per_block;
@@ -753,8 +802,9 @@ CePlan ce_plan(int T, int H, int V, bool grad, int sms) {
   q.acc = take(static_cast<size_t>(q.acc_rows) * H * 4);
   q.per_block = o;
   o *= q.blocks;
-  q.raised = take(static_cast<size_t>(q.pieces) * 4);
-  q.packed = take(rows * H * 2);
+  q.raised = take(static_cast<size_t>(q.pieces) * 8);
+  q.ld_packed = (H + BK - 1) / BK * BK;  // rows on whole 128-byte lines, whatever h's stride
+  q.packed = take(rows * q.ld_packed * 2);
   q.part_s = take(static_cast<size_t>(q.tiles) * rows * 4);
   q.part_r = take(static_cast<size_t>(q.tiles) * rows * 4);
   q.p = take(grad ? rows * q.piece_tiles * TILE * 2 : 0);
@@ -824,7 +874,7 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
   uint16_t* P = reinterpret_cast<uint16_t*>(ws + q.p);
   const long long ldp = static_cast<long long>(q.piece_tiles) * TILE;
   CeGemm a{}, b{};
-  if (!tma_encode_sw128(&a.ta, packed, false, H, q.tcap, 2ull * H, BK, 128) ||
+  if (!tma_encode_sw128(&a.ta, packed, false, H, q.tcap, 2ull * q.ld_packed, BK, 128) ||
       !tma_encode_sw128(&a.tb, w, false, H, V, 2ull * ldw, BK, 128) ||
       (grad && (!tma_encode_sw128(&a.to, P, false, ldp, q.tcap, 2ull * ldp, BK, 128) ||
                 !tma_encode_sw128(&b.tb, w, false, H, V, 2ull * ldw, 64, BK))))
@@ -845,12 +895,18 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
     int* n_rows = reinterpret_cast<int*>(base + q.n_rows);
     float* acc = reinterpret_cast<float*>(base + q.acc);
     CE_CK(launch(ce_prepare_kernel, n, row_threads(H), 0, st, h + t0 * ldh, ldh, w, ldw, n, H, V, t1 + t0,
-                 t2 ? t2 + t0 : nullptr, packed, rows, reinterpret_cast<int*>(base + q.place), n_rows, q.splits, raised,
+                 t2 ? t2 + t0 : nullptr, packed, q.ld_packed, rows, reinterpret_cast<int*>(base + q.place), n_rows, q.splits, raised,
                  q.pieces,
                  lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr, err));
     if (grad && !tma_encode_sw128(&b.to, acc, true, H, static_cast<unsigned long long>(q.acc_rows), 4ull * H, 32, 128))
       return cudaErrorInvalidValue;
+    const CeStats stats{q.tiles, q.tcap, part_s, part_r, rows, lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr};
+    b.stats = stats;
     a.n_rows = b.n_rows = n_rows;
+    a.P = P;
+    a.ldp = ldp;
+    a.acc_cols = H;
+    a.row_ref = rows.ref;
     a.target = rows.target;
     a.ref = rows.ref;
     for (int i = 0; i < q.pieces; ++i) {
@@ -859,17 +915,16 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
       a.tile0 = tile0;
       a.w_row0 = b.w_row0 = tile0 * TILE;
       a.cols = std::min(V - a.w_row0, a.n_tiles * TILE);
-      a.raised = raised + i;
+      a.raised = raised + 2 * i;
+      a.acc = i > 0 ? acc : nullptr;
       CE_CK(launch(ce_gemm_kernel<false>, 2 * std::min(q.pairs, mt * a.n_tiles), THREADS, SMEM_BYTES, st, a));
       if (!grad) continue;
-      CE_CK(launch(ce_raise_kernel, 64, 256, 0, st, raised + i, n_rows, a.tile0, a.n_tiles, q.tcap, part_r,
-                   rows.ref, P, ldp, acc, H, i > 0));
       b.kb = (a.cols + BK - 1) / BK;
       b.accumulate = i > 0;
+      b.with_stats = i == q.pieces - 1;
       CE_CK(launch(ce_gemm_kernel<true>, 2 * q.pairs, THREADS, SMEM_BYTES, st, b));
     }
-    CE_CK(launch(ce_stats_kernel, (n + STATS_ROWS - 1) / STATS_ROWS, 32 * STATS_ROWS, 0, st, n_rows, q.tiles, q.tcap, part_s, part_r, rows,
-                 lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr));
+    if (!grad) CE_CK(launch(ce_stats_kernel, (n + 3) / 4, 128, 0, st, n_rows, stats));
   }
   return cudaSuccess;
 }
@@ -877,10 +932,11 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
 cudaError_t linear_ce_bwd_launch(const uint16_t* w, long long ldw, int T, int H, int V, const float* weight,
                                  const float* weight2, uint16_t* dh, long long ldd, uint8_t* ws, cudaStream_t st) {
   const CePlan q = ce_plan(T, H, V, true, device_sm_count());
+  const int threads = std::max(256, row_threads(H));
   for (int k = 0; k < q.blocks; ++k) {
     const int t0 = k * q.block, n = std::min(q.block, T - t0);
     uint8_t* base = ws + k * q.per_block;
-    CE_CK(launch(ce_dh_kernel, n, row_threads(H), 0, st, reinterpret_cast<int*>(base + q.place), rows_of(q, base),
+    CE_CK(launch(ce_dh_kernel, n, threads, threads * 32, st, reinterpret_cast<int*>(base + q.place), rows_of(q, base),
                  weight + t0, weight2 ? weight2 + t0 : nullptr, reinterpret_cast<float*>(base + q.acc),
                  reinterpret_cast<int*>(base + q.n_rows), w, ldw, H, dh + t0 * ldd, ldd));
   }
