@@ -145,8 +145,7 @@ __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.laun
 // the clock rises under the power limit when fewer work.  Measured, 1 / 2 / 3 ranges: 1108 / 901 / 977 us
 // at 512 x 4096 x 128256 (32 tiles on 74 pairs), 1691 / 1720 / 1734 at 1024, 2700 / 2530 / 2490 at 1500,
 // 6566 / 6430 / 6683 at 2048 x 8192, 1793 / 1842 / 1908 at 4096 x 2048 x 64000.
-inline int grad_splits(int m_tiles, int H, int pairs, int kb_first) {
-  const int tiles = m_tiles * ((H + TILE - 1) / TILE);
+inline int grad_splits(int m_tiles, int H, int tiles, int pairs, int kb_first) {
   const long long room = ACC_BYTES / (4ll * TILE * H) / (m_tiles < 1 ? 1 : m_tiles);
   const int most = room < MAX_SPLITS ? static_cast<int>(room) : MAX_SPLITS;
   int best = 1;
@@ -189,20 +188,29 @@ __device__ __forceinline__ Unit unit_of(const CeGemm& p, int m_tiles, int splits
 // Rows that met a logit beyond their ref's room: P of this piece and the accumulators go to the
 // largest ref a part took.  Powers of two: exact.  By the piece's last CTA, a warp a row; rare (a target
 // 2^80 times less likely than another token), so one CTA is enough.
-__device__ __noinline__ void raise_rows(const CeGemm& p, int rows, int m_tiles, int splits) {
+struct Raise {
+  const float* part_r;  // of the piece's first part
+  int parts, width, tcap;  // width: columns of a part
+  float* row_ref;
+  uint16_t* P;
+  long long ldp;
+  float* acc;  // the gradient's accumulators, if earlier pieces are in them
+  int acc_cols, m_tiles, splits;
+};
+__device__ __noinline__ void raise_rows(const Raise& p, int rows) {
   const int lane = threadIdx.x & 31;
   for (int r = threadIdx.x >> 5; r < rows; r += THREADS / 32) {
     const float before = __ldcg(p.row_ref + r);
     float top = before;
-    for (int i = lane; i < p.n_tiles; i += 32) top = fmaxf(top, __ldcg(p.part_r + static_cast<long long>(p.tile0 + i) * p.tcap + r));
+    for (int i = lane; i < p.parts; i += 32) top = fmaxf(top, __ldcg(p.part_r + static_cast<long long>(i) * p.tcap + r));
     top = warp_max(top);
     if (!(top > before)) continue;
-    for (int i = 0; i < p.n_tiles; ++i) {
-      const float have = __ldcg(p.part_r + static_cast<long long>(p.tile0 + i) * p.tcap + r);
+    for (int i = 0; i < p.parts; ++i) {
+      const float have = __ldcg(p.part_r + static_cast<long long>(i) * p.tcap + r);
       if (have == top) continue;
       const float f = exp2f(have - top);
-      uint16_t* q = p.P + r * p.ldp + i * TILE;
-      for (int c = lane; c < TILE; c += 32) {
+      uint16_t* q = p.P + r * p.ldp + i * p.width;
+      for (int c = lane; c < p.width; c += 32) {
         const __nv_bfloat16 v = __float2bfloat16_rn(bf16_to_f32(__ldcg(q + c)) * f);
         q[c] = *reinterpret_cast<const uint16_t*>(&v);
       }
@@ -211,12 +219,27 @@ __device__ __noinline__ void raise_rows(const CeGemm& p, int rows, int m_tiles, 
       const float f = exp2f(before - top);
       const int m = r / TILE;
       for (int c = lane; c < p.acc_cols; c += 32)
-        for (int j = 0; j < splits; ++j)
-          p.acc[(static_cast<long long>(j * m_tiles + m) * TILE + r % TILE) * p.acc_cols + c] *= f;
+        for (int j = 0; j < p.splits; ++j)
+          p.acc[(static_cast<long long>(j * p.m_tiles + m) * TILE + r % TILE) * p.acc_cols + c] *= f;
     }
     __syncwarp();
     if (lane == 0) p.row_ref[r] = top;
   }
+}
+
+// Counts the CTAs done with a piece; true in all threads of the last one if a row was raised: what the
+// others wrote is then there to be read.
+__device__ __forceinline__ bool last_of_piece(int* raised, volatile int* slot) {
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const bool last = atomicAdd(raised + 1, 1) == static_cast<int>(gridDim.x) - 1;
+    __threadfence();
+    *slot = last && __ldcg(raised) != 0;
+  }
+  __syncthreads();
+  if (!*slot) return false;
+  fence_proxy_async_all();
+  return true;
 }
 
 // One row's sums of parts, log-probs and lse, by a warp: parts are added a lane each in a fixed order, the
@@ -559,20 +582,295 @@ done:
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
-  if (!GRAD && p.store_p) {
-    volatile int* is_last = abort_flag + 1;
-    if (threadIdx.x == 0) {
-      __threadfence();
-      *is_last = atomicAdd(p.raised + 1, 1) == static_cast<int>(gridDim.x) - 1;
-      __threadfence();
-    }
-    __syncthreads();
-    if (*is_last && __ldcg(p.raised)) {
-      fence_proxy_async_all();
-      raise_rows(p, rows, m_tiles, p.n_rows[1]);
-      fence_proxy_async_all();
+  if (!GRAD && p.store_p && last_of_piece(p.raised, abort_flag + 1))
+    raise_rows(Raise{p.part_r + static_cast<long long>(p.tile0) * p.tcap, p.n_tiles, TILE, p.tcap, p.row_ref, p.P, p.ldp, p.acc,
+                     p.acc_cols, m_tiles, p.n_rows[1]},
+               rows);
+}
+
+// ---------------------------------------------------------------- few rows
+// Up to 128 rows of the batch: the roles of the operands are turned round, 128 rows of W against the N rows of the
+// batch (N a multiple of 16), so that no tile is mostly padding.  One CTA each (M = 128); an epilogue thread holds
+// one row of W, and sums over W's rows are reduced across lanes.
+// GRAD = false: 128 columns of the vocabulary -> P, sums.  GRAD = true: 128 columns of dh, over a range of the
+// vocabulary -> accumulator of the range.
+// Bound by W, which is read for either product, where hidden and vocabulary are large: measured against the
+// wide tiles at 84 rows x 3640 x 92004 NARROW_84, at 63 x 200 x 115150 NARROW_63 us.
+struct CeNarrow {
+  CUtensorMap ta, tb;  // W; the batch's rows: packed hidden states, or P
+  const int* n_rows;   // as CeGemm
+  int N;               // rows of the batch, rounded up to 16
+  int n_tiles, kb;
+  int cols;            // vocabulary, or columns of dh
+  const int2* target;
+  const float* ref;
+  float *part_s, *part_r;  // [128 columns of the vocabulary][tcap]
+  int tcap, store_p;
+  int* raised;
+  uint16_t* P;
+  long long ldp;
+  float* row_ref;
+  float* acc;
+  int with_stats;
+  CeStats stats;
+  int* err;
+};
+constexpr int NARROW = 128;  // rows of W of a tile, and most rows of the batch
+constexpr int NARROW_TABLES = NARROW * (4 + 4 + 8) + 4 * NARROW * 4;  // refs, a tile's own refs, targets, sums of four warps
+constexpr int NARROW_SMEM = STAGES * 2 * OPERAND + NARROW_TABLES + BARRIERS + 1024;
+
+// Sums of 16 columns over a warp's lanes: after it, lane 2 i + (0 or 1) has column bit-reversed(i)'s.
+__device__ __forceinline__ float reduce16(float (&s)[16], int lane) {
+#pragma unroll
+  for (int n = 8, o = 16; n >= 1; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = up ? s[i] : s[i + n], keep = up ? s[i + n] : s[i];
+      s[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
     }
   }
+  return s[0] + __shfl_xor_sync(0xffffffffu, s[0], 1);
+}
+
+template <bool GRAD>
+__global__ void __launch_bounds__(THREADS, 1) ce_narrow_kernel(const __grid_constant__ CeNarrow p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float* refs = reinterpret_cast<float*>(smem + STAGES * 2 * OPERAND);
+  float* tile_refs = refs + NARROW;
+  int2* targets = reinterpret_cast<int2*>(tile_refs + NARROW);
+  float* sums = reinterpret_cast<float*>(targets + NARROW);  // [4][NARROW]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sums + 4 * NARROW);
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;
+  uint64_t* acc_empty = acc_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_launch();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);  // eight epilogue warps
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, 2 * NARROW);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  const int rows = *p.n_rows, splits = GRAD ? p.n_rows[1] : 1;
+  const int units = rows > 0 ? p.n_tiles * splits : 0;
+  if (!GRAD && threadIdx.x < NARROW) {
+    const int t = threadIdx.x;
+    refs[t] = t < rows ? p.ref[t] : 0.f;
+    targets[t] = t < rows ? p.target[t] : make_int2(-1, -1);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto range = [&](int u, int& tile, int& share, int& lo, int& hi) {
+    tile = u % p.n_tiles;
+    share = u / p.n_tiles;
+    lo = GRAD ? static_cast<int>(static_cast<long long>(p.kb) * share / splits) : 0;
+    hi = GRAD ? static_cast<int>(static_cast<long long>(p.kb) * (share + 1) / splits) : p.kb;
+  };
+  int tile, share, lo, hi;
+
+  if (warp == 0) {
+    // ---- operand loads
+    const bool issues = elect_one();
+    uint32_t s = 0, phase = 1;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      range(u, tile, share, lo, hi);
+      for (int kb = lo; kb < hi; ++kb) {
+        if (!mbar_wait_warp(&empty[s], phase, abort_flag, p.err)) goto done;
+        if (issues) {
+          uint8_t* a = smem + s * 2 * OPERAND;
+          mbar_arrive_expect_tx(&full[s], OPERAND + p.N * 128);
+          if (GRAD) {
+            tma_load_2d(a, &p.ta, tile * NARROW, kb * BK, &full[s]);
+            tma_load_2d(a + 8192, &p.ta, tile * NARROW + 64, kb * BK, &full[s]);
+          } else {
+            tma_load_2d(a, &p.ta, kb * BK, tile * NARROW, &full[s]);
+          }
+          tma_load_2d(a + OPERAND, &p.tb, kb * BK, 0, &full[s]);
+        }
+        __syncwarp();
+        if (++s == STAGES) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---- products
+    const bool issues = elect_one();
+    const uint32_t idesc = idesc_bf16(NARROW, p.N, GRAD, false), base = smem_u32(smem);
+    const uint64_t da0 = GRAD ? sw128_mnmajor_desc(base) : sw128_kmajor_desc(base);
+    const uint64_t db0 = sw128_kmajor_desc(base + OPERAND);
+    uint32_t s = 0, phase = 0, b = 0, b_phase = 1;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      range(u, tile, share, lo, hi);
+      for (int kb = lo; kb < hi;) {
+        const int stop = GRAD ? hi : min(hi, kb + CHUNK);
+        if (!mbar_wait_warp(&acc_empty[b], b_phase, abort_flag, p.err)) goto done;
+        uint32_t more = 0;
+        for (; kb < stop; ++kb) {
+          if (!mbar_wait_warp(&full[s], phase, abort_flag, p.err)) goto done;
+          tc_fence_after();
+          if (issues) {
+            const uint64_t da = da0 + s * (2 * OPERAND >> 4), db = db0 + s * (2 * OPERAND >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              tc_mma_f16(tmem + b * NARROW, da + k * ((GRAD ? 2048 : 32) >> 4), db + k * (32 >> 4), idesc, more);
+              more = 1;
+            }
+            tc_commit(&empty[s]);
+          }
+          __syncwarp();
+          more = 1;
+          if (++s == STAGES) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (issues) tc_commit(&acc_full[b]);
+        __syncwarp();
+        b ^= 1;
+        if (b == 0) b_phase ^= 1;
+      }
+    }
+  } else if (GRAD && warp == 3) {
+    if (p.with_stats)
+      for (int r = blockIdx.x; r < rows; r += gridDim.x) row_stats(p.stats, r);
+  } else if (warp >= 4) {
+    // ---- epilogue: thread = row of W; two groups of four warps take every other 16 rows of the batch
+    const int group = (warp - 4) >> 2, quarter = warp & 3, of_row = quarter * 32 + lane, blocks = p.N / 16;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    int n_done = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      range(u, tile, share, lo, hi);
+      if (lo == hi) continue;
+      const int col = tile * NARROW + of_row;  // of the vocabulary, or of dh
+      const bool live = col < p.cols;
+      uint32_t l[4][16];
+      for (int kb = lo; kb < hi; kb += GRAD ? hi - lo : CHUNK) {
+        const int buf = n_done & 1;
+        if (!epilogue_all(mbar_wait_bounded(&acc_full[buf], (n_done >> 1) & 1, abort_flag, p.err))) goto done;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (2 * i + group >= blocks) continue;
+          uint32_t v[16];
+          tmem_ld16(tmem + lanes + buf * NARROW + (2 * i + group) * 16, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) l[i][j] = __float_as_uint((kb > lo ? __uint_as_float(l[i][j]) : 0.f) + __uint_as_float(v[j]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        ++n_done;
+      }
+      if (GRAD) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t0 = (2 * i + group) * 16;
+          float* out = p.acc + (static_cast<long long>(share) * TILE + t0) * p.cols + col;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (live && t0 + j < rows) out[static_cast<long long>(j) * p.cols] = __uint_as_float(l[i][j]);
+        }
+        continue;
+      }
+      // columns that stay out: targets, looked for only where one is in this tile
+      bool here = false;
+      for (int t = lane; t < rows; t += 32)
+        here = here || (targets[t].x / NARROW == tile && targets[t].x >= 0) || (targets[t].y / NARROW == tile && targets[t].y >= 0);
+      here = __any_sync(0xffffffffu, here);
+      auto out_of_it = [&](int t) { return !live || (here && (targets[t].x == col || targets[t].y == col)); };
+      const int own = threadIdx.x - 128;  // the row of the batch whose sums this thread joins
+      for (int attempt = 0; attempt < 2; ++attempt) {
+        const float* against = attempt ? tile_refs : refs;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t0 = (2 * i + group) * 16;
+          if (t0 >= p.N) continue;
+          float e[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            e[j] = out_of_it(t0 + j) ? 0.f : exp2_approx(fmaf(__uint_as_float(l[i][j]), LOG2E, -against[t0 + j]));
+            if (p.store_p && t0 + j < rows) {
+              const __nv_bfloat16 v = __float2bfloat16_rn(e[j]);
+              p.P[static_cast<long long>(t0 + j) * p.ldp + col] = *reinterpret_cast<const uint16_t*>(&v);
+            }
+          }
+          const float sum = reduce16(e, lane);
+          const int c = (lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane >> 1 & 1);
+          if ((lane & 1) == 0) sums[quarter * NARROW + t0 + c] = sum;
+        }
+        epilogue_all(true);
+        float total = 0.f;
+        if (own < rows) total = (sums[own] + sums[NARROW + own]) + (sums[2 * NARROW + own] + sums[3 * NARROW + own]);
+        const bool over = own < rows && total > REF_ROOM;
+        if (epilogue_all(!over) || attempt == 1) {
+          if (own < rows) {
+            const long long at = static_cast<long long>(tile) * p.tcap + own;
+            p.part_s[at] = total;
+            p.part_r[at] = against[own];
+          }
+          break;
+        }
+        // a logit far above its row's ref: once more, against the largest logit here
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t0 = (2 * i + group) * 16;
+          if (t0 >= p.N) continue;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float top = warp_max(out_of_it(t0 + j) ? -INFINITY : __uint_as_float(l[i][j]));
+            if (lane == 0) sums[quarter * NARROW + t0 + j] = top;
+          }
+        }
+        epilogue_all(true);
+        if (own < NARROW) {
+          float ref = refs[own];
+          if (over) {
+            const float top = fmaxf(fmaxf(sums[own], sums[NARROW + own]), fmaxf(sums[2 * NARROW + own], sums[3 * NARROW + own]));
+            ref = ceilf(top * LOG2E);
+            *p.raised = 1;
+          }
+          tile_refs[own] = ref;
+        }
+        epilogue_all(true);
+      }
+    }
+  }
+done:
+  __syncwarp();
+  if (*abort_flag) {  // a wait gave up: let this CTA's copies in flight land before its memory goes
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * NARROW);
+  }
+  if (!GRAD && p.store_p && last_of_piece(p.raised, abort_flag + 1))
+    raise_rows(Raise{p.part_r, p.n_tiles, NARROW, p.tcap, p.row_ref, p.P, p.ldp, nullptr, 0, 1, 1}, rows);
 }
 
 // ---------------------------------------------------------------- rows
@@ -750,7 +1048,8 @@ constexpr long long P_BYTES = 96ll << 20; // of one piece's P: half of the L2
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct CePlan {
-  int pairs, block, blocks, tcap, tiles, piece_tiles, pieces, h_tiles, kb_first;
+  int pairs, block, blocks, tcap, tiles, parts, piece_tiles, pieces, h_tiles, kb_first;
+  bool narrow;  // few rows: ce_narrow_kernel
   long long acc_rows, ld_packed;
   Splits splits;
   // byte offsets: per row block (stride per_block), then shared by the blocks
@@ -768,16 +1067,20 @@ CePlan ce_plan(int T, int H, int V, bool grad, int sms) {
   q.h_tiles = (H + TILE - 1) / TILE;
   const int mt = q.tcap / TILE;
   q.piece_tiles = q.tiles;
+  // W is not walked in pieces there, so P has to fit
+  q.narrow = T <= NARROW && (!grad || 2ll * NARROW * q.tiles * TILE <= P_BYTES);
+  q.parts = q.narrow ? (V + NARROW - 1) / NARROW : q.tiles;
   if (grad) {
     // a piece's tiles fill whole waves of CTA pairs, as many as P's bytes allow
     const long long most = std::max(1ll, P_BYTES / (static_cast<long long>(q.tcap) * TILE * 2));
     long long n = std::min<long long>(most, q.tiles);
     const long long waves = n * mt / q.pairs;
     if (waves >= 1 && n < q.tiles) n = waves * q.pairs / mt;
-    q.piece_tiles = static_cast<int>(std::max(1ll, n));
+    if (!q.narrow) q.piece_tiles = static_cast<int>(std::max(1ll, n));
     q.kb_first = (std::min(V, q.piece_tiles * TILE) + BK - 1) / BK;
     for (int m = 0; m <= mt; ++m) {
-      q.splits.of[m] = grad_splits(m, H, q.pairs, q.kb_first);
+      q.splits.of[m] = q.narrow ? (m ? grad_splits(1, H, (H + NARROW - 1) / NARROW, 2 * q.pairs, q.kb_first) : 1)
+                               : grad_splits(m, H, m * q.h_tiles, q.pairs, q.kb_first);
       q.acc_rows = std::max(q.acc_rows, static_cast<long long>(TILE) * m * q.splits.of[m]);
     }
   }
@@ -805,9 +1108,9 @@ CePlan ce_plan(int T, int H, int V, bool grad, int sms) {
   q.raised = take(static_cast<size_t>(q.pieces) * 8);
   q.ld_packed = (H + BK - 1) / BK * BK;  // rows on whole 128-byte lines, whatever h's stride
   q.packed = take(rows * q.ld_packed * 2);
-  q.part_s = take(static_cast<size_t>(q.tiles) * rows * 4);
-  q.part_r = take(static_cast<size_t>(q.tiles) * rows * 4);
-  q.p = take(grad ? rows * q.piece_tiles * TILE * 2 : 0);
+  q.part_s = take(static_cast<size_t>(q.parts) * rows * 4);
+  q.part_r = take(static_cast<size_t>(q.parts) * rows * 4);
+  q.p = take(grad ? (q.narrow ? NARROW : rows) * q.piece_tiles * TILE * 2 : 0);
   q.total = o;
   return q;
 }
@@ -854,6 +1157,8 @@ cudaError_t gemm_attributes() {
   if (done.load() & bit) return cudaSuccess;
   CE_CK(cudaFuncSetAttribute(ce_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
   CE_CK(cudaFuncSetAttribute(ce_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
+  CE_CK(cudaFuncSetAttribute(ce_narrow_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, NARROW_SMEM));
+  CE_CK(cudaFuncSetAttribute(ce_narrow_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, NARROW_SMEM));
   done.fetch_or(bit);
   return cudaSuccess;
 }
@@ -876,7 +1181,7 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
   CeGemm a{}, b{};
   if (!tma_encode_sw128(&a.ta, packed, false, H, q.tcap, 2ull * q.ld_packed, BK, 128) ||
       !tma_encode_sw128(&a.tb, w, false, H, V, 2ull * ldw, BK, 128) ||
-      (grad && (!tma_encode_sw128(&a.to, P, false, ldp, q.tcap, 2ull * ldp, BK, 128) ||
+      (grad && (!tma_encode_sw128(&a.to, P, false, ldp, q.narrow ? NARROW : q.tcap, 2ull * ldp, BK, 128) ||
                 !tma_encode_sw128(&b.tb, w, false, H, V, 2ull * ldw, 64, BK))))
     return cudaErrorInvalidValue;
   b.ta = a.to;
@@ -900,7 +1205,7 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
                  lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr, err));
     if (grad && !tma_encode_sw128(&b.to, acc, true, H, static_cast<unsigned long long>(q.acc_rows), 4ull * H, 32, 128))
       return cudaErrorInvalidValue;
-    const CeStats stats{q.tiles, q.tcap, part_s, part_r, rows, lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr};
+    const CeStats stats{q.parts, q.tcap, part_s, part_r, rows, lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr};
     b.stats = stats;
     a.n_rows = b.n_rows = n_rows;
     a.P = P;
@@ -909,7 +1214,41 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
     a.row_ref = rows.ref;
     a.target = rows.target;
     a.ref = rows.ref;
-    for (int i = 0; i < q.pieces; ++i) {
+    if (q.narrow) {
+      const int N = (n + 15) / 16 * 16;
+      CeNarrow c{}, d{};
+      if (!tma_encode_sw128(&c.tb, packed, false, H, q.tcap, 2ull * q.ld_packed, BK, static_cast<unsigned>(N)) ||
+          (grad && !tma_encode_sw128(&d.tb, P, false, ldp, NARROW, 2ull * ldp, BK, static_cast<unsigned>(N))))
+        return cudaErrorInvalidValue;
+      c.ta = a.tb;
+      c.n_rows = d.n_rows = n_rows;
+      c.N = d.N = N;
+      c.n_tiles = q.parts;
+      c.kb = a.kb;
+      c.cols = V;
+      c.target = rows.target;
+      c.ref = c.row_ref = rows.ref;
+      c.part_s = part_s;
+      c.part_r = part_r;
+      c.tcap = q.tcap;
+      c.store_p = grad;
+      c.raised = raised;
+      c.P = P;
+      c.ldp = ldp;
+      c.err = d.err = err;
+      CE_CK(launch(ce_narrow_kernel<false>, std::min(2 * q.pairs, c.n_tiles), THREADS, NARROW_SMEM, st, c));
+      if (grad) {
+        d.ta = b.tb;
+        d.n_tiles = (H + NARROW - 1) / NARROW;
+        d.kb = (V + BK - 1) / BK;
+        d.cols = H;
+        d.acc = acc;
+        d.with_stats = 1;
+        d.stats = stats;
+        CE_CK(launch(ce_narrow_kernel<true>, 2 * q.pairs, THREADS, NARROW_SMEM, st, d));
+      }
+    }
+    for (int i = 0; i < q.pieces && !q.narrow; ++i) {
       const int tile0 = i * q.piece_tiles;
       a.n_tiles = std::min(q.piece_tiles, q.tiles - tile0);
       a.tile0 = tile0;

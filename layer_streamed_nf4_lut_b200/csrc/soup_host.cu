@@ -1699,7 +1699,9 @@ soup_status create_model(const soup_model_config* cfg, const soup_model_options*
       alloc_into(m, m->roww2, T) || alloc_into(m, m->seqw, 256) || alloc_into(m, m->scal, 64))
     return fail(SOUP_ERR_OOM);
   if (opt && opt->loss_in_pieces) {
-    // a step has any number of rows up to max_tokens: the largest need of all
+    // a step has any number of rows up to max_tokens: the largest need of all (it changes every 256 rows, and
+    // once at 128)
+    m->ce_ws_bytes = linear_ce_workspace(static_cast<int>(std::min<size_t>(128, T)), c.hidden, c.vocab, true);
     for (size_t t = std::min<size_t>(256, T);; t = std::min(t + 256, T)) {
       m->ce_ws_bytes = std::max(m->ce_ws_bytes, linear_ce_workspace(static_cast<int>(t), c.hidden, c.vocab, true));
       if (t == T) break;
