@@ -594,8 +594,9 @@ done:
 // one row of W, and sums over W's rows are reduced across lanes.
 // GRAD = false: 128 columns of the vocabulary -> P, sums.  GRAD = true: 128 columns of dh, over a range of the
 // vocabulary -> accumulator of the range.
-// Bound by W, which is read for either product, where hidden and vocabulary are large: measured against the
-// wide tiles at 84 rows x 3640 x 92004 NARROW_84, at 63 x 200 x 115150 NARROW_63 us.
+// Bound by W, which is read for either product, where hidden and vocabulary are large.  Measured with gradient,
+// against the wide tiles: 370 / 421 us at 128 rows x 4096 x 128256, 240 / 293 at 84 x 3640 x 92004 (W alone: 204
+// for two readings), 62 / 79 at 63 x 200 x 115150, 34 / 50 at 3 x 904 x 25621, 25.6 / 29.7 at 64 x 256 x 1024.
 struct CeNarrow {
   CUtensorMap ta, tb;  // W; the batch's rows: packed hidden states, or P
   const int* n_rows;   // as CeGemm
@@ -619,7 +620,7 @@ constexpr int NARROW = 128;  // rows of W of a tile, and most rows of the batch
 constexpr int NARROW_TABLES = NARROW * (4 + 4 + 8) + 4 * NARROW * 4;  // refs, a tile's own refs, targets, sums of four warps
 constexpr int NARROW_SMEM = STAGES * 2 * OPERAND + NARROW_TABLES + BARRIERS + 1024;
 
-// Sums of 16 columns over a warp's lanes: after it, lane 2 i + (0 or 1) has column bit-reversed(i)'s.
+// Sums of 16 columns over a warp's lanes: after it, lane 2 c + (0 or 1) has column c's.
 __device__ __forceinline__ float reduce16(float (&s)[16], int lane) {
 #pragma unroll
   for (int n = 8, o = 16; n >= 1; n >>= 1, o >>= 1) {
@@ -798,7 +799,15 @@ __global__ void __launch_bounds__(THREADS, 1) ce_narrow_kernel(const __grid_cons
       for (int t = lane; t < rows; t += 32)
         here = here || (targets[t].x / NARROW == tile && targets[t].x >= 0) || (targets[t].y / NARROW == tile && targets[t].y >= 0);
       here = __any_sync(0xffffffffu, here);
-      auto out_of_it = [&](int t) { return !live || (here && (targets[t].x == col || targets[t].y == col)); };
+      if (here || (tile + 1) * NARROW > p.cols) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int2 tg = targets[((2 * i + group) * 16 + j) & (NARROW - 1)];
+            if (!live || tg.x == col || tg.y == col) l[i][j] = 0xff800000u;  // -inf
+          }
+      }
       const int own = threadIdx.x - 128;  // the row of the batch whose sums this thread joins
       for (int attempt = 0; attempt < 2; ++attempt) {
         const float* against = attempt ? tile_refs : refs;
@@ -808,16 +817,18 @@ __global__ void __launch_bounds__(THREADS, 1) ce_narrow_kernel(const __grid_cons
           if (t0 >= p.N) continue;
           float e[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            e[j] = out_of_it(t0 + j) ? 0.f : exp2_approx(fmaf(__uint_as_float(l[i][j]), LOG2E, -against[t0 + j]));
-            if (p.store_p && t0 + j < rows) {
-              const __nv_bfloat16 v = __float2bfloat16_rn(e[j]);
-              p.P[static_cast<long long>(t0 + j) * p.ldp + col] = *reinterpret_cast<const uint16_t*>(&v);
+          for (int j = 0; j < 16; ++j) e[j] = exp2_approx(fmaf(__uint_as_float(l[i][j]), LOG2E, -against[t0 + j]));
+          if (p.store_p) {
+            uint16_t* out = p.P + static_cast<long long>(t0) * p.ldp + col;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2, out += 2 * p.ldp) {
+              const uint32_t two = pack_bf16x2(e[j], e[j + 1]);
+              if (t0 + j < rows) *out = static_cast<uint16_t>(two);
+              if (t0 + j + 1 < rows) out[p.ldp] = static_cast<uint16_t>(two >> 16);
             }
           }
           const float sum = reduce16(e, lane);
-          const int c = (lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2 + (lane >> 1 & 1);
-          if ((lane & 1) == 0) sums[quarter * NARROW + t0 + c] = sum;
+          if ((lane & 1) == 0) sums[quarter * NARROW + t0 + (lane >> 1)] = sum;
         }
         epilogue_all(true);
         float total = 0.f;
@@ -838,7 +849,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_narrow_kernel(const __grid_cons
           if (t0 >= p.N) continue;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float top = warp_max(out_of_it(t0 + j) ? -INFINITY : __uint_as_float(l[i][j]));
+            const float top = warp_max(__uint_as_float(l[i][j]));
             if (lane == 0) sums[quarter * NARROW + t0 + j] = top;
           }
         }

@@ -95,6 +95,29 @@ def test_loss_and_gradient(T, H, V, counted):
     check_ce(h, w, t1)  # without a gradient
 
 
+@pytest.mark.parametrize("T", [3, 15, 16, 17, 112, 127, 128, 129])
+@pytest.mark.parametrize("H,V", [(128, 127), (264, 384), (2200, 1025)])
+def test_few_rows(T, H, V):
+    """Up to 128 rows run with the operands' roles turned round; around its borders, two targets among them."""
+    h, w, t1, weight = ce_inputs(T, H, V, 20 + T + V, 0.9)
+    t2 = torch.randint(0, V, (T,), generator=gen(21), device="cuda", dtype=torch.int32)
+    t2 = torch.where(torch.rand(T, generator=gen(22), device="cuda") < 0.3, t2, -1).int()
+    check_ce(h, w, t1, weight, t2, 0.5 * weight)
+    check_ce(h, w, t1)
+
+
+@pytest.mark.parametrize("T", [100, 300])
+def test_few_and_many_rows_with_logits_far_above(T):
+    """Single columns far above the target, in a tile of the vocabulary each, so that tiles of one row have refs of
+    their own."""
+    H, V = 128, 1500
+    h, w, t1, weight = ce_inputs(T, H, V, 23, sure=False)
+    for k, col in enumerate((5, 300, 700, 1499)):
+        w[col] = (h[k].float() * (0.5 + 0.3 * k)).bfloat16()  # l = 64 .. 180 for row k
+        t1[k] = 1000
+    check_ce(h, w, t1, weight)
+
+
 def test_several_pieces_and_blocks_of_rows():
     # 4096 rows take pieces of the vocabulary; rows past them a second walk over it
     h, w, t1, weight = ce_inputs(4096, 64, 21000, 3)
