@@ -393,7 +393,7 @@ soup_status soup_linear_ce_bwd(const void* w, long long ldw, int T, int hidden, 
  * lr, 1/(1-b1^step), 1/(1-b2^step) read on the device in place of lr and step, for captured graphs.
  * tensors is a host array, read during the call; tensors do not overlap.  A tensor of n = 0 is allowed.
  * |g| is below 10^17: v' times 2^24 c has to fit in fp32.  SOUP_ERR_INVALID_ARG
- * for null pointers, n < 0, step < 1 (without hp), v_scale without m_scale or the reverse, a
+ * for null pointers, n < 0, step < 1 (without hp), betas outside [0, 1), eps < 0, v_scale without m_scale or the reverse, a
  * state address not 32-byte aligned, or tensors not aligned to their own type. */
 #define SOUP_ADAMW_BLOCK 256
 typedef struct soup_adamw_tensor {

@@ -242,55 +242,65 @@ __device__ __forceinline__ bool last_of_piece(int* raised, volatile int* slot) {
   return true;
 }
 
-// One row's sums of parts, log-probs and lse, by a warp: parts are added a lane each in a fixed order, the
-// lanes and the row's scalars in 64 bits, the logarithms side by side in three lanes.
-__device__ __noinline__ void row_stats(const CeStats& q, int r) {
+// Log-probs and lse of the rows first, first + step, ... by a warp: each row's parts are added a lane each
+// in a fixed order and the lanes in 64 bits; then a lane forms a row's scalars in 64 bits (7000 clocks of
+// dependent instructions, so 32 rows at one time).
+__device__ __noinline__ void rows_stats(const CeStats& q, int first, int step, int rows) {
   const int lane = threadIdx.x & 31;
-  float top = q.rows.ref[r], sum = 0.f;
-  // eight parts at a time, so that their loads are in flight together
-  for (int i = lane; i < q.parts; i += 8 * 32) {
-    float s[8], k[8];
+  for (long long base = first; base < rows; base += 32ll * step) {
+    float my_top = 0.f;
+    double other = 0.0;
+    for (int k = 0; k < 32 && base + static_cast<long long>(k) * step < rows; ++k) {
+      const int r = static_cast<int>(base) + k * step;
+      float top = q.rows.ref[r], sum = 0.f;
+      // eight parts at a time, so that their loads are in flight together
+      for (int i = lane; i < q.parts; i += 8 * 32) {
+        float s[8], ref[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int part = i + j * 32;
-      const long long at = static_cast<long long>(part) * q.tcap + r;
-      s[j] = part < q.parts ? q.part_s[at] : 0.f;
-      k[j] = part < q.parts ? q.part_r[at] : top;
-    }
+        for (int j = 0; j < 8; ++j) {
+          const int part = i + j * 32;
+          const long long at = static_cast<long long>(part) * q.tcap + r;
+          s[j] = part < q.parts ? q.part_s[at] : 0.f;
+          ref[j] = part < q.parts ? q.part_r[at] : top;
+        }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (k[j] > top) {
-        sum *= exp2f(top - k[j]);
-        top = k[j];
+        for (int j = 0; j < 8; ++j) {
+          if (ref[j] > top) {
+            sum *= exp2f(top - ref[j]);
+            top = ref[j];
+          }
+          sum += ref[j] == top ? s[j] : s[j] * exp2f(ref[j] - top);
+        }
       }
-      sum += k[j] == top ? s[j] : s[j] * exp2f(k[j] - top);
-    }
-  }
-  const float own = top;
-  top = warp_max(top);
-  double other = static_cast<double>(sum);
-  if (own != top) other *= exp2(static_cast<double>(own - top));
+      const float own = top;
+      top = warp_max(top);
+      double all = static_cast<double>(own == top ? sum : sum * exp2f(own - top));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) other += __shfl_xor_sync(0xffffffffu, other, o);
-  const int2 tg = q.rows.target[r];
-  const bool two = tg.y >= 0 && tg.y != tg.x;
-  const double ln2 = 0.6931471805599453;
-  // lane 1: the second target, the others the first
-  const double mine = static_cast<double>(lane == 1 ? q.rows.lb[r] : q.rows.la[r]) - top;
-  const double e = lane == 1 && !two ? 0.0 : exp2(mine);
-  const double ea = __shfl_sync(0xffffffffu, e, 0), eb = __shfl_sync(0xffffffffu, e, 1);
-  const double z = other + ea + eb, rest = other + (lane == 1 ? ea : eb);  // of the lane's own target
-  // lane 2: log z (z is at least about 0.5: the largest term lies within a power of two of its ref)
-  const double l = log1p(lane == 2 ? z - 1.0 : rest / e);
-  const double lz = __shfl_sync(0xffffffffu, l, 2);
-  const double lp = e > rest ? -l : mine * ln2 - lz;
-  const double lpa = __shfl_sync(0xffffffffu, lp, 0), lpb = __shfl_sync(0xffffffffu, lp, 1);
-  const int t = q.rows.row[r];
-  if (lane < 2) (lane ? q.rows.pb : q.rows.pa)[r] = make_float2(static_cast<float>(e / z), static_cast<float>(rest / z));
-  if (lane == 2) q.rows.inv_z[r] = static_cast<float>(1.0 / z);
-  if (lane == 3 && q.lse) q.lse[t] = static_cast<float>(static_cast<double>(top) * ln2 + lz);
-  if (lane == 4) q.logp[t] = static_cast<float>(lpa);
-  if (lane == 5 && q.logp2) q.logp2[t] = tg.y >= 0 ? static_cast<float>(two ? lpb : lpa) : 0.f;
+      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      if (lane == k) {
+        my_top = top;
+        other = all;
+      }
+    }
+    if (base + static_cast<long long>(lane) * step >= rows) continue;
+    const int r = static_cast<int>(base) + lane * step;
+    const int2 tg = q.rows.target[r];
+    const bool two = tg.y >= 0 && tg.y != tg.x;
+    const double ln2 = 0.6931471805599453;
+    const double a = static_cast<double>(q.rows.la[r]) - my_top, b = static_cast<double>(q.rows.lb[r]) - my_top;
+    const double ea = exp2(a), eb = two ? exp2(b) : 0.0;
+    const double z = other + ea + eb, lz = log(z);
+    const double rest_a = other + eb, rest_b = other + ea;
+    const double lpa = ea > rest_a ? -log1p(rest_a / ea) : a * ln2 - lz;
+    const double lpb = two ? (eb > rest_b ? -log1p(rest_b / eb) : b * ln2 - lz) : lpa;
+    q.rows.inv_z[r] = static_cast<float>(1.0 / z);
+    q.rows.pa[r] = make_float2(static_cast<float>(ea / z), static_cast<float>(rest_a / z));
+    q.rows.pb[r] = make_float2(static_cast<float>(eb / z), static_cast<float>(rest_b / z));
+    const int t = q.rows.row[r];
+    if (q.lse) q.lse[t] = static_cast<float>(static_cast<double>(my_top) * ln2 + lz);
+    q.logp[t] = static_cast<float>(lpa);
+    if (q.logp2) q.logp2[t] = tg.y >= 0 ? static_cast<float>(lpb) : 0.f;
+  }
 }
 
 // 256 x 256 tiles, one CTA pair each (tcgen05 cta_group::2, M = 256, N = 256), two accumulators
@@ -421,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
   } else if (GRAD && warp == 3) {
     // ---- the log-probs, beside the last piece's products
     if (p.with_stats)
-      for (int r = blockIdx.x; r < rows; r += gridDim.x) row_stats(p.stats, r);
+      rows_stats(p.stats, blockIdx.x, gridDim.x, rows);
   } else if (warp >= 4) {
     // ---- epilogue: thread = accumulator row; two groups of four warps take half of the columns each
     const int group = (warp - 4) >> 2;
@@ -753,7 +763,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_narrow_kernel(const __grid_cons
     }
   } else if (GRAD && warp == 3) {
     if (p.with_stats)
-      for (int r = blockIdx.x; r < rows; r += gridDim.x) row_stats(p.stats, r);
+      rows_stats(p.stats, blockIdx.x, gridDim.x, rows);
   } else if (warp >= 4) {
     // ---- epilogue: thread = row of W; two groups of four warps take every other 16 rows of the batch
     const int group = (warp - 4) >> 2, quarter = warp & 3, of_row = quarter * 32 + lane, blocks = p.N / 16;
@@ -913,6 +923,7 @@ __global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh,
   if (threadIdx.x == 0) before = 0;
   __syncthreads();
   int n = 0;
+  #pragma unroll 4
   for (int i = threadIdx.x; i < t; i += blockDim.x) n += targets_of(t1, t2, i, V, nullptr).x >= 0;
   n = __reduce_add_sync(0xffffffffu, n);
   if ((threadIdx.x & 31) == 0 && n) atomicAdd(&before, n);
@@ -971,7 +982,7 @@ __global__ void __launch_bounds__(128) ce_stats_kernel(const int* __restrict__ n
   pdl_launch();
   pdl_wait();
   const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (r < *n_rows) row_stats(q, r);
+  rows_stats(q, r, gridDim.x * 4, *n_rows);
 }
 
 // dh of one row of the batch per block: the accumulators of the tile's shares, added in order, and the

@@ -116,6 +116,13 @@ def test_adamw_refusals():
     assert adam([], m=None, v=None) == OK and adam([(None, None, None, 0)], m=None, v=None) == OK  # nothing to do
 
 
+@pytest.mark.parametrize("b1,b2,eps", [(1.0, 0.999, 1e-8), (-0.1, 0.999, 1e-8), (0.9, 1.0, 1e-8), (0.9, float("nan"), 1e-8),
+                                       (0.9, 0.999, -1e-8), (0.9, 0.999, float("nan"))])
+def test_adamw_options(b1, b2, eps):
+    o = _lib.AdamwOptions(0, 0, 1, 1e-3, b1, b2, eps, 0.0)
+    assert L.soup_adamw_multi(tensors((A, A, None, 5)), 1, ctypes.byref(o), A, A, None, None, None, None) == INVALID
+
+
 def test_adamw_state_sizes():
     n = ctypes.c_longlong()
     assert L.soup_adamw_state_numel(tensors((A, A, None, 1), (A, A, None, 0), (A, A, None, 256), (A, A, None, 257)), 4,
