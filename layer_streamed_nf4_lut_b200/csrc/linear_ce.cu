@@ -96,6 +96,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
 // Orders what the async proxy (TMA) and ordinary accesses do to global memory.
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ bool elect_one() {
@@ -339,6 +342,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 16);  // eight epilogue warps in each CTA
     }
+    prefetch_map(&p.ta);
+    prefetch_map(&p.tb);
+    if (GRAD || p.store_p) prefetch_map(&p.to);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -670,6 +676,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_narrow_kernel(const __grid_cons
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 8);  // eight epilogue warps
     }
+    prefetch_map(&p.ta);
+    prefetch_map(&p.tb);
     *abort_flag = 0;
     mbar_fence_init();
   }
