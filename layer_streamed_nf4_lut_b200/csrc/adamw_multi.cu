@@ -12,11 +12,12 @@
 //
 // Bound by HBM: p is read and written, g read, the states read and written: 28 B per element with
 // fp32 throughout, 16 B with 8-bit states.  A warp works one block (8 elements a lane), so a scale
-// is one warp reduction, and finds its tensor from a short table.  A warp for each block, taken up in order by the
-// hardware, measured better than persistent warps with runs of 1 to 70 blocks (what is in flight then lies
-// together, which keeps DRAM pages open): 674 against 697 to 830 us at 168 M elements with fp32 throughout
-// (6.97 TB/s), 450 us (5.98 TB/s) with 8-bit states, where the arithmetic of the codes comes near to the
-// memory's time: 450 instructions a block, so conversions and divisions are kept out of it.
+// is one warp reduction, and finds its tensor from a short table.  A warp for each block, taken up in order by
+// the hardware, measured better than persistent warps with runs of 1 to 70 blocks (what is in flight then lies
+// together, which keeps DRAM pages open): 676 against 697 to 830 us at 168 M elements with fp32 throughout
+// (6.95 TB/s).  With 8-bit states it takes 435 us (6.2 TB/s); the arithmetic of the codes, 640 instructions a block
+// at 80 % of the issue slots, comes near to the memory's time, so conversions, divisions and correctly
+// rounded roots are kept out of it where they can be.
 #include "common.cuh"
 #include "internal.h"
 

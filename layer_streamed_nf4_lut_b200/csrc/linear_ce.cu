@@ -15,11 +15,16 @@
 // (the target's logit, rounded): a rescaling by a difference of two refs is a power of two and
 // therefore exact.  bf16 has the exponent range of fp32, so ref need not be the row's
 // maximum, only within REF_ROOM powers of two below it; a tile that finds a larger logit stores its
-// values against a ref of its own and raises a flag, and `ce_raise_kernel` brings the row's P and
+// values against a ref of its own and raises a flag, and the piece's last CTA brings the row's P and
 // accumulator to the larger ref before the second GEMM reads them.
 //
+// Bound by the tensor cores, and back to back by the power limit: 2048 x 8192 x 128256 takes 5.52 ms on its
+// own (1.56 PFLOP/s) and 6.4 ms in a loop (1.35), 512 x 4096 x 128256 758 and 900 us (1.42, 1.20); the
+// tensor pipe is active 93 % of the time.  Small sizes are bound by their chain of four kernels (prepare,
+// logits, gradient with the log-probs, dh), each set up while the one before ends: 22 us at 64 x 256 x 1024.
+//
 // Rows without a target (target < 0) take no part: `ce_prepare_kernel` packs the others' hidden
-// states, so a half-masked batch costs half.
+// states (onto whole 128-byte lines), so a half-masked batch costs half.
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
