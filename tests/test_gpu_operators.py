@@ -462,3 +462,117 @@ def test_rope_rows_past_32_bits_of_offset():
     assert torch.equal(a, b)
     M.rope(q, None, pos, inplace=True)
     assert torch.equal(q, b) and int((buf[256:wide] != 0).sum()) == 0
+
+
+# ------------------------------------------------------------------ how calls may be made
+def test_calls_refuse_wrong_tensors():
+    from layer_streamed_nf4_lut_b200 import model as M
+
+    def refused(f, *a, **kw):
+        with pytest.raises(M.SoupError) as e:
+            f(*a, **kw)
+        assert e.value.status in (-1, -7), e.value
+
+    h, w, t1, weight = ce_inputs(6, 64, 90, 1)
+    refused(M.linear_ce, h.float(), w, t1)
+    refused(M.linear_ce, h, w[:, :56], t1)
+    refused(M.linear_ce, h, w, t1.long())
+    refused(M.linear_ce, h, w, t1[:5])
+    refused(M.linear_ce, h, w, t1, weight.double())
+    refused(M.linear_ce, h, w, t1, None, t1, weight)  # weights for the second targets alone
+    refused(M.linear_ce, h.t().contiguous().t(), w, t1)
+    refused(M.linear_ce, h[:, :60], w[:, :60], t1)  # hidden not a multiple of 8
+    refused(M.linear_ce, h[:, 4:60], w[:, 4:60], t1)  # rows not 16-byte aligned
+    fwd = M.linear_ce_fwd(h, w, t1)
+    refused(M.linear_ce_bwd, w[:80], fwd["saved"], weight)
+    refused(M.linear_ce_bwd, w, fwd["saved"], weight[:3])
+    assert "saved" not in M.linear_ce_fwd(h, w, t1, grad=False)
+    p, g = torch.zeros(300, device="cuda"), torch.zeros(300, device="cuda")
+    s = M.adamw_state([300], 8)
+    refused(M.adamw_multi, [p], [g[:299]], lr=1.0, step=1, **s)
+    refused(M.adamw_multi, [p[::2]], [g[::2]], lr=1.0, step=1, **M.adamw_state([150], 8))
+    refused(M.adamw_multi, [p.double()], [g], lr=1.0, step=1, **s)
+    refused(M.adamw_multi, [p, p.bfloat16()], [g, g], lr=1.0, step=1, **M.adamw_state([300, 300], 8))
+    refused(M.adamw_multi, [p], [g], lr=1.0, step=1, **M.adamw_state([600], 8))
+    refused(M.adamw_multi, [p], [g], lr=1.0, step=0, **s)
+    refused(M.adamw_multi, [p], [g], lr=1.0, step=1, betas=(0.9, 1.0), **s)
+    refused(M.adamw_multi, [p], [g], lr=1.0, step=1, m=s["m"], v=s["v"])  # coded states without their scales
+    pos = torch.arange(4, device="cuda", dtype=torch.int32)
+    q = torch.zeros(4, 2, 64, device="cuda")
+    refused(M.rope, q.half(), None, pos)
+    refused(M.rope, q, None, pos.long())
+    refused(M.rope, q, None, pos[:3])
+    refused(M.rope, q, q.bfloat16(), pos)
+    refused(M.rope, q.transpose(0, 1), None, pos[:2])
+    refused(M.rope, q, None, pos, rotary_dim=66)
+
+
+def test_rotation_and_update_on_another_stream_and_captured():
+    from layer_streamed_nf4_lut_b200 import model as M
+    pos = torch.arange(500, device="cuda", dtype=torch.int32)
+    q = torch.randn(500, 6, 128, generator=gen(1), device="cuda").bfloat16()
+    want, _ = M.rope(q, None, pos)
+    sizes = [1000, 7, 40000]
+    start, grad = torch.randn(sum(sizes), generator=gen(2), device="cuda"), torch.randn(sum(sizes), generator=gen(3), device="cuda")
+    a, sa = start.clone(), M.adamw_state(sizes, 8)
+    M.adamw_multi(list(a.split(sizes)), list(grad.split(sizes)), lr=1e-2, step=1, **sa)
+    b, sb = start.clone(), M.adamw_state(sizes, 8)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got, _ = M.rope(q, None, pos)
+        M.adamw_multi(list(b.split(sizes)), list(grad.split(sizes)), lr=1e-2, step=1, **sb)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(a, b) and all(torch.equal(sa[k], sb[k]) for k in sa)
+    b.copy_(start)
+    for k in sb:
+        sb[k].zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, _ = M.rope(q, None, pos)
+        M.adamw_multi(list(b.split(sizes)), list(grad.split(sizes)), lr=1e-2, step=1, **sb)
+    got.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(a, b) and all(torch.equal(sa[k], sb[k]) for k in sa)
+
+
+def test_rotation_of_nothing():
+    from layer_streamed_nf4_lut_b200 import model as M
+    pos = torch.zeros(0, device="cuda", dtype=torch.int32)
+    q, k = M.rope(torch.zeros(0, 4, 64, device="cuda"), torch.zeros(0, 2, 64, device="cuda"), pos)
+    assert q.shape == (0, 4, 64) and k.shape == (0, 2, 64)
+    one = torch.zeros(1, device="cuda", dtype=torch.int32)
+    q, k = M.rope(torch.zeros(1, 0, 64, device="cuda"), torch.ones(1, 2, 64, device="cuda"), one)
+    assert q.shape == (1, 0, 64) and (k == 1).all()  # position 0 turns nothing
+
+
+def test_two_graphs_of_the_loss_do_not_share_a_workspace():
+    from layer_streamed_nf4_lut_b200 import model as M
+    a, b = ce_inputs(200, 256, 900, 31), ce_inputs(60, 128, 700, 32)
+    want = [M.linear_ce(*x) for x in (a, b)]
+    graphs, got = [], []
+    for x in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(M.linear_ce(*x))
+        graphs.append(g)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, (s1, s2)):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert all(torch.equal(x[k], y[k]) for k in y)
+
+
+def test_accumulated_gradients_of_the_same_index_twice():
+    """The same rows, target and position given twice: each result is that of the row alone."""
+    from layer_streamed_nf4_lut_b200 import model as M
+    h, w, t1, weight = ce_inputs(40, 128, 600, 33)
+    one = M.linear_ce(h, w, t1, weight)
+    two = M.linear_ce(torch.cat((h, h)), w, torch.cat((t1, t1)), torch.cat((weight, weight)))
+    for k in one:
+        assert torch.equal(two[k][:40], one[k]) and torch.equal(two[k][40:], one[k]), k

@@ -219,3 +219,27 @@ def test_model_options():
     assert L.soup_model_create_with(None, None, None, ctypes.byref(out)) == INVALID
     f = L.soup_model_set_lora_adam8
     assert f(None, A, A, A, A, A, A) == INVALID
+
+
+# ------------------------------------------------------------------ the calls on tensors
+def refused(f, *a, **kw):
+    with pytest.raises(M.SoupError) as e:
+        f(*a, **kw)
+    return e.value.status
+
+
+def test_calls_refuse_what_is_not_on_a_gpu():
+    import torch
+    h, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(10, 64, dtype=torch.bfloat16)
+    t, x = torch.zeros(4, dtype=torch.int32), torch.zeros(4)
+    assert refused(M.linear_ce, h, w, t) == INVALID and refused(M.linear_ce, h, w, t, x) == INVALID
+    assert refused(M.linear_ce, None, w, t) == INVALID and refused(M.linear_ce_fwd, h, w, [0, 1, 2, 3]) == INVALID
+    assert refused(M.linear_ce_bwd, w, None, x) == INVALID
+    s = M.adamw_state([4], 8, device="cpu")
+    assert refused(M.adamw_multi, [x], [x], lr=1e-3, step=1, **s) == INVALID
+    assert refused(M.adamw_multi, [x], [], lr=1e-3, step=1, **s) == INVALID
+    assert M.adamw_multi([], [], lr=1e-3, step=1, **s) is None  # nothing to do
+    assert refused(M.adamw_state_values, **s) == INVALID
+    assert refused(M.rope, h.view(4, 1, 64), None, t) == INVALID
+    with pytest.raises(TypeError):
+        M.adamw_multi(3, [x], lr=1e-3, step=1, **s)
