@@ -141,6 +141,19 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
       : "memory");
   return all != 0;
 }
+// The same of one group of four.
+__device__ __forceinline__ bool group_all(int group, bool ok) {
+  int all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %2, 0;\n\t"
+      "bar.red.and.pred q, %1, 128, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(1 + group), "r"(static_cast<int>(ok))
+      : "memory");
+  return all != 0;
+}
 // Barrier of one group of four epilogue warps.
 __device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
 // Programmatic dependent launch: a kernel may be set up while the one before it ends; it touches
@@ -320,7 +333,13 @@ __device__ __noinline__ void rows_stats(const CeStats& q, int first, int step, i
 // zero, and over 8192 products that moved lse by 1.4e-6 of itself and log-probs by 3.4e-6.  In chunks of
 // 4096 / 2048 / 1024: lse 7e-7 / 3.2e-7 / 1.6e-7 (fp32 sums on the ordinary cores: 8e-7), at 5764 / 5774 / 5816
 // us for 2048 x 8192 x 128256.  An accumulator is also free again as soon as it is read, before the exponentials.
-template <bool GRAD>
+//
+// SHORT (logits of one chunk, hidden up to 2048): a tile's epilogue takes longer than its products, 10000 to 14000
+// clocks with both groups of warps on one tile and in step.  The groups then take every other tile each, the
+// one's loads from tensor memory and stores beside the other's exponentials: 117 us against 130 at
+// 1608 x 208 x 26757, 151 / 162 at 512 x 512 x 100000, 252 / 258 at 2000 x 1024 x 32000, 399 / 404 at
+// 1024 x 2048 x 64000, and without gradient 132 / 155 at 4000 x 400 x 30000.
+template <bool GRAD, bool SHORT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_kernel(const __grid_constant__ CeGemm p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -345,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 16);  // eight epilogue warps in each CTA
+      mbar_init(&acc_empty[b], SHORT ? 8 : 16);  // the epilogue warps of both CTAs that read it
     }
     prefetch_map(&p.ta);
     prefetch_map(&p.tb);
@@ -443,6 +462,99 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
     // ---- the log-probs, beside the last piece's products
     if (p.with_stats)
       rows_stats(p.stats, blockIdx.x, gridDim.x, rows);
+  } else if (SHORT && warp >= 4) {
+    // ---- epilogue: thread = accumulator row; two groups of four warps take every other tile each
+    const int group = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * TILE;
+    uint8_t* box = staging + group * 16384;
+    uint8_t* my_row = box + row * 128;
+    const bool elected = (threadIdx.x & 127) == 0;
+    uint32_t phase = 0;
+    for (int u = pair + group * pairs; u < units; u += 2 * pairs, phase ^= 1) {
+      const Unit t = unit_of<GRAD>(p, m_tiles, splits, u);
+      const int m0 = t.m * TILE + rank * 128, r = m0 + row;
+      const bool live = r < rows;
+      const int2 tg = live ? p.target[r] : make_int2(-1, -1);
+      float ref = live ? p.ref[r] : 0.f, total = 0.f;
+      if (!group_all(group, mbar_wait_bounded(&acc_full[group], phase, abort_flag, p.err))) goto done;
+      tc_fence_after();
+      uint32_t l[GROUP];
+      // logits of half the columns; those that stay out are the targets', for the few rows that have one here, and
+      // those past the end
+      auto fetch = [&](int n0, int from) {
+#pragma unroll
+        for (int c = 0; c < GROUP; c += 32) tmem_ld32(acc + from + c, l + c);
+        tmem_ld_wait();
+        const int ta = tg.x - p.w_row0 - n0, tb = tg.y - p.w_row0 - n0, valid = p.cols - n0;
+        if (__any_sync(0xffffffffu, (ta >= 0 && ta < GROUP) || (tb >= 0 && tb < GROUP)) || valid < GROUP) {
+#pragma unroll
+          for (int j = 0; j < GROUP; ++j)
+            if (j == ta || j == tb || j >= valid) l[j] = 0xff800000u;  // -inf
+        }
+      };
+      for (int attempt = 0; attempt < 2; ++attempt) {
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int from = 0; from < TILE; from += GROUP) {
+          const int n0 = t.n * TILE + from;
+          fetch(n0, from);
+#pragma unroll
+          for (int c = 0; c < GROUP; c += 64) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 64; j += 2) {
+              const float e0 = exp2_approx(fmaf(__uint_as_float(l[c + j]), LOG2E, -ref));
+              const float e1 = exp2_approx(fmaf(__uint_as_float(l[c + j + 1]), LOG2E, -ref));
+              sum[j & 3] += e0;
+              sum[(j + 1) & 3] += e1;
+              w[j >> 1] = pack_bf16x2(e0, e1);
+            }
+            if (p.store_p) {
+              if (elected) tma_store_wait_read<0>();
+              group_sync(group);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(my_row + ((j ^ (row & 7)) << 4)) =
+                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+              fence_proxy_async_smem();
+              group_sync(group);
+              if (elected) {
+                tma_store_2d(&p.to, n0 + c, m0, box);
+                tma_store_commit();
+              }
+            }
+          }
+        }
+        total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // A logit far above ref (an infinite sum counts): once more, against the row's largest logit here
+        const bool over = live && total > REF_ROOM;
+        if (group_all(group, !over) || attempt == 1) break;
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int from = 0; from < TILE; from += GROUP) {
+          fetch(t.n * TILE + from, from);
+#pragma unroll
+          for (int j = 0; j < GROUP; ++j) top = fmaxf(top, __uint_as_float(l[j]));
+        }
+        if (elected) tma_store_wait_all();  // the box is written again: in order
+        group_sync(group);
+        if (over) {
+          ref = ceilf(top * LOG2E);
+          *p.raised = 1;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[group], 0));
+      const long long at = static_cast<long long>(p.tile0 + t.n) * p.tcap + r;
+      p.part_s[at] = total;
+      p.part_r[at] = ref;
+    }
+    if (elected) {
+      tma_store_wait_all();
+      fence_proxy_async_all();  // P may be read and written again below
+    }
   } else if (warp >= 4) {
     // ---- epilogue: thread = accumulator row; two groups of four warps take half of the columns each
     const int group = (warp - 4) >> 2;
@@ -1190,8 +1302,9 @@ cudaError_t gemm_attributes() {
   CE_CK(cudaGetDevice(&dev));
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (done.load() & bit) return cudaSuccess;
-  CE_CK(cudaFuncSetAttribute(ce_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
-  CE_CK(cudaFuncSetAttribute(ce_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
+  CE_CK(cudaFuncSetAttribute(ce_gemm_kernel<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
+  CE_CK(cudaFuncSetAttribute(ce_gemm_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
+  CE_CK(cudaFuncSetAttribute(ce_gemm_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES));
   CE_CK(cudaFuncSetAttribute(ce_narrow_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, NARROW_SMEM));
   CE_CK(cudaFuncSetAttribute(ce_narrow_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, NARROW_SMEM));
   done.fetch_or(bit);
@@ -1291,12 +1404,13 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
       a.cols = std::min(V - a.w_row0, a.n_tiles * TILE);
       a.raised = raised + 2 * i;
       a.acc = i > 0 ? acc : nullptr;
-      CE_CK(launch(ce_gemm_kernel<false>, 2 * std::min(q.pairs, mt * a.n_tiles), THREADS, SMEM_BYTES, st, a));
+      CE_CK(launch(a.kb <= CHUNK ? ce_gemm_kernel<false, true> : ce_gemm_kernel<false, false>,
+                   2 * std::min(q.pairs, mt * a.n_tiles), THREADS, SMEM_BYTES, st, a));
       if (!grad) continue;
       b.kb = (a.cols + BK - 1) / BK;
       b.accumulate = i > 0;
       b.with_stats = i == q.pieces - 1;
-      CE_CK(launch(ce_gemm_kernel<true>, 2 * q.pairs, THREADS, SMEM_BYTES, st, b));
+      CE_CK(launch(ce_gemm_kernel<true, false>, 2 * q.pairs, THREADS, SMEM_BYTES, st, b));
     }
     if (!grad) CE_CK(launch(ce_stats_kernel, (n + 3) / 4, 128, 0, st, n_rows, stats));
   }
