@@ -48,7 +48,7 @@ constexpr int STAGING = 2 * 16384;   // epilogue: a box of 128 rows x 128 bytes 
 constexpr int BARRIERS = 256;
 constexpr int JOIN = 2 * 128 * 4;    // epilogue: the second group's sums, for the first one
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING + BARRIERS + JOIN + 1024;
-constexpr int THREADS = 384;         // warp 0 TMA, 1 MMA, 2 TMEM, 3 log-probs, 4-11 epilogue
+constexpr int THREADS = 384;         // warp 0 TMA, 1 MMA, 2 TMEM and log-probs, 3 log-probs, 4-11 epilogue
 constexpr int MAX_SPLITS = 80;
 constexpr long long ACC_BYTES = 144ll << 20; // of all accumulators, unless one for each tile takes more
 constexpr float LOG2E = 1.4426950408889634f;
@@ -269,11 +269,12 @@ __device__ __forceinline__ bool last_of_piece(int* raised, volatile int* slot) {
 __device__ __noinline__ void rows_stats(const CeStats& q, int first, int step, int rows) {
   const int lane = threadIdx.x & 31;
   for (long long base = first; base < rows; base += 32ll * step) {
-    float my_top = 0.f;
+    const long long own_row = base + static_cast<long long>(lane) * step;
+    float my_top = own_row < rows ? q.rows.ref[own_row] : 0.f;
     double other = 0.0;
     for (int k = 0; k < 32 && base + static_cast<long long>(k) * step < rows; ++k) {
       const int r = static_cast<int>(base) + k * step;
-      float top = q.rows.ref[r], sum = 0.f;
+      float top = __shfl_sync(0xffffffffu, my_top, k), sum = 0.f;
       // eight parts at a time, so that their loads are in flight together
       for (int i = lane; i < q.parts; i += 8 * 32) {
         float s[8], ref[8];
@@ -303,8 +304,8 @@ __device__ __noinline__ void rows_stats(const CeStats& q, int first, int step, i
         other = all;
       }
     }
-    if (base + static_cast<long long>(lane) * step >= rows) continue;
-    const int r = static_cast<int>(base) + lane * step;
+    if (own_row >= rows) continue;
+    const int r = static_cast<int>(own_row);
     const int2 tg = q.rows.target[r];
     const bool two = tg.y >= 0 && tg.y != tg.x;
     const double ln2 = 0.6931471805599453;
@@ -458,10 +459,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
         if (b == 0) b_phase ^= 1;
       }
     }
-  } else if (GRAD && warp == 3) {
+  } else if (GRAD && (warp == 2 || warp == 3)) {
     // ---- the log-probs, beside the last piece's products
-    if (p.with_stats)
-      rows_stats(p.stats, blockIdx.x, gridDim.x, rows);
+    if (p.with_stats) rows_stats(p.stats, 2 * blockIdx.x + warp - 2, 2 * gridDim.x, rows);
   } else if (SHORT && warp >= 4) {
     // ---- epilogue: thread = accumulator row; two groups of four warps take every other tile each
     const int group = (warp - 4) >> 2;
@@ -479,50 +479,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
       float ref = live ? p.ref[r] : 0.f, total = 0.f;
       if (!group_all(group, mbar_wait_bounded(&acc_full[group], phase, abort_flag, p.err))) goto done;
       tc_fence_after();
-      uint32_t l[GROUP];
-      // logits of half the columns; those that stay out are the targets', for the few rows that have one here, and
-      // those past the end
-      auto fetch = [&](int n0, int from) {
+      const int n0 = t.n * TILE, ta = tg.x - p.w_row0 - n0, tb = tg.y - p.w_row0 - n0;  // the targets' columns here
+      // columns that stay out: the targets', for the few rows that have one here, and those past the end
+      const bool masks = __any_sync(0xffffffffu, (ta >= 0 && ta < TILE) || (tb >= 0 && tb < TILE)) || n0 + TILE > p.cols;
+      auto mask = [&](uint32_t (&l)[32], int c) {
 #pragma unroll
-        for (int c = 0; c < GROUP; c += 32) tmem_ld32(acc + from + c, l + c);
-        tmem_ld_wait();
-        const int ta = tg.x - p.w_row0 - n0, tb = tg.y - p.w_row0 - n0, valid = p.cols - n0;
-        if (__any_sync(0xffffffffu, (ta >= 0 && ta < GROUP) || (tb >= 0 && tb < GROUP)) || valid < GROUP) {
-#pragma unroll
-          for (int j = 0; j < GROUP; ++j)
-            if (j == ta || j == tb || j >= valid) l[j] = 0xff800000u;  // -inf
-        }
+        for (int j = 0; j < 32; ++j)
+          if (c + j == ta || c + j == tb || n0 + c + j >= p.cols) l[j] = 0xff800000u;  // -inf
       };
       for (int attempt = 0; attempt < 2; ++attempt) {
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t even[32], odd[32], w[32];
+        auto part = [&](uint32_t (&l)[32], int c, uint32_t* out) {
+          if (masks) mask(l, c);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float e0 = exp2_approx(fmaf(__uint_as_float(l[j]), LOG2E, -ref));
+            const float e1 = exp2_approx(fmaf(__uint_as_float(l[j + 1]), LOG2E, -ref));
+            sum[j & 3] += e0;
+            sum[(j + 1) & 3] += e1;
+            out[j >> 1] = pack_bf16x2(e0, e1);
+          }
+        };
+        // 32 columns are on their way while the exponentials of those before are formed
+        tmem_ld32(acc, even);
 #pragma unroll 1
-        for (int from = 0; from < TILE; from += GROUP) {
-          const int n0 = t.n * TILE + from;
-          fetch(n0, from);
+        for (int c = 0; c < TILE; c += 64) {
+          tmem_ld_wait32(even);
+          tmem_ld32(acc + c + 32, odd);
+          part(even, c, w);
+          tmem_ld_wait32(odd);
+          if (c + 64 < TILE) tmem_ld32(acc + c + 64, even);
+          part(odd, c + 32, w + 16);
+          if (p.store_p) {
+            if (elected) tma_store_wait_read<0>();
+            group_sync(group);
 #pragma unroll
-          for (int c = 0; c < GROUP; c += 64) {
-            uint32_t w[32];
-#pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-              const float e0 = exp2_approx(fmaf(__uint_as_float(l[c + j]), LOG2E, -ref));
-              const float e1 = exp2_approx(fmaf(__uint_as_float(l[c + j + 1]), LOG2E, -ref));
-              sum[j & 3] += e0;
-              sum[(j + 1) & 3] += e1;
-              w[j >> 1] = pack_bf16x2(e0, e1);
-            }
-            if (p.store_p) {
-              if (elected) tma_store_wait_read<0>();
-              group_sync(group);
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(my_row + ((j ^ (row & 7)) << 4)) =
-                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-              fence_proxy_async_smem();
-              group_sync(group);
-              if (elected) {
-                tma_store_2d(&p.to, n0 + c, m0, box);
-                tma_store_commit();
-              }
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(my_row + ((j ^ (row & 7)) << 4)) =
+                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            fence_proxy_async_smem();
+            group_sync(group);
+            if (elected) {
+              tma_store_2d(&p.to, n0 + c, m0, box);
+              tma_store_commit();
             }
           }
         }
@@ -532,10 +532,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) ce_gemm_
         if (group_all(group, !over) || attempt == 1) break;
         float top = -INFINITY;
 #pragma unroll 1
-        for (int from = 0; from < TILE; from += GROUP) {
-          fetch(t.n * TILE + from, from);
+        for (int c = 0; c < TILE; c += 32) {
+          tmem_ld32(acc + c, even);
+          tmem_ld_wait32(even);
+          if (masks) mask(even, c);
 #pragma unroll
-          for (int j = 0; j < GROUP; ++j) top = fmaxf(top, __uint_as_float(l[j]));
+          for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(even[j]));
         }
         if (elected) tma_store_wait_all();  // the box is written again: in order
         group_sync(group);
@@ -887,8 +889,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_narrow_kernel(const __grid_cons
       }
     }
   } else if (GRAD && warp == 3) {
-    if (p.with_stats)
-      rows_stats(p.stats, blockIdx.x, gridDim.x, rows);
+    if (p.with_stats) rows_stats(p.stats, blockIdx.x, gridDim.x, rows);
   } else if (warp >= 4) {
     // ---- epilogue: thread = row of W; two groups of four warps take every other 16 rows of the batch
     const int group = (warp - 4) >> 2, quarter = warp & 3, of_row = quarter * 32 + lane, blocks = p.N / 16;
@@ -1047,9 +1048,17 @@ __global__ void ce_prepare_kernel(const uint16_t* __restrict__ h, long long ldh,
   pdl_wait();
   if (threadIdx.x == 0) before = 0;
   __syncthreads();
-  int n = 0;
-  #pragma unroll 4
-  for (int i = threadIdx.x; i < t; i += blockDim.x) n += targets_of(t1, t2, i, V, nullptr).x >= 0;
+  int n = 0, counted = 0;
+  if (((reinterpret_cast<uintptr_t>(t1) | reinterpret_cast<uintptr_t>(t2)) & 15u) == 0) {
+    for (int i = threadIdx.x; i < t / 4; i += blockDim.x) {
+      const int4 a = reinterpret_cast<const int4*>(t1)[i];
+      const int4 b = t2 ? reinterpret_cast<const int4*>(t2)[i] : make_int4(-1, -1, -1, -1);
+      n += (a.x >= 0 && a.x < V && b.x < V) + (a.y >= 0 && a.y < V && b.y < V) + (a.z >= 0 && a.z < V && b.z < V) +
+           (a.w >= 0 && a.w < V && b.w < V);
+    }
+    counted = t / 4 * 4;
+  }
+  for (int i = counted + threadIdx.x; i < t; i += blockDim.x) n += targets_of(t1, t2, i, V, nullptr).x >= 0;
   n = __reduce_add_sync(0xffffffffu, n);
   if ((threadIdx.x & 31) == 0 && n) atomicAdd(&before, n);
   if (t == 0)
@@ -1347,7 +1356,7 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
     const CeRows rows = rows_of(q, base);
     int* n_rows = reinterpret_cast<int*>(base + q.n_rows);
     float* acc = reinterpret_cast<float*>(base + q.acc);
-    CE_CK(launch(ce_prepare_kernel, n, row_threads(H), 0, st, h + t0 * ldh, ldh, w, ldw, n, H, V, t1 + t0,
+    CE_CK(launch(ce_prepare_kernel, n, std::max(64, row_threads(H)), 0, st, h + t0 * ldh, ldh, w, ldw, n, H, V, t1 + t0,
                  t2 ? t2 + t0 : nullptr, packed, q.ld_packed, rows, reinterpret_cast<int*>(base + q.place), n_rows, q.splits, raised,
                  q.pieces,
                  lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr, err));
@@ -1420,10 +1429,11 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
 cudaError_t linear_ce_bwd_launch(const uint16_t* w, long long ldw, int T, int H, int V, const float* weight,
                                  const float* weight2, uint16_t* dh, long long ldd, uint8_t* ws, cudaStream_t st) {
   const CePlan q = ce_plan(T, H, V, true, device_sm_count());
-  const int threads = std::max(256, row_threads(H));
   for (int k = 0; k < q.blocks; ++k) {
     const int t0 = k * q.block, n = std::min(q.block, T - t0);
     uint8_t* base = ws + k * q.per_block;
+    // many accumulators a row: threads to share them
+    const int threads = q.splits.of[(n + TILE - 1) / TILE] > 2 ? std::max(256, row_threads(H)) : row_threads(H);
     CE_CK(launch(ce_dh_kernel, n, threads, threads * 32, st, reinterpret_cast<int*>(base + q.place), rows_of(q, base),
                  weight + t0, weight2 ? weight2 + t0 : nullptr, reinterpret_cast<float*>(base + q.acc),
                  reinterpret_cast<int*>(base + q.n_rows), w, ldw, H, dh + t0 * ldd, ldd));
