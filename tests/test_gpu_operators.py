@@ -183,6 +183,18 @@ def test_logits_far_above_the_target(T, V):
     check_ce(h, w, t1, weight)
 
 
+@pytest.mark.parametrize("T,V", [(300, 1500), (4096, 13000)])
+def test_long_rows_with_logits_far_above_the_target(T, V):
+    """The same where a logit is added up in several chunks."""
+    H = 2312
+    h, w, t1, weight = ce_inputs(T, H, V, 34, 0.9, sure=False)
+    h[::3] *= 100  # logits of about +-100 and, below, +-200 and more
+    w[V // 2:] *= 2
+    w[V - 3] *= 2
+    check_ce(h, w, t1, weight)
+    check_ce(h, w, t1)
+
+
 def test_a_row_of_nan_stays_alone():
     from layer_streamed_nf4_lut_b200 import model as M
     h, w, t1, weight = ce_inputs(50, 64, 400, 12)
