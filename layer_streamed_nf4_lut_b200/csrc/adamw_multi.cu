@@ -20,6 +20,7 @@
 // rounded roots are kept out of it where they can be.
 #include "common.cuh"
 #include "internal.h"
+#include "pdl.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -185,6 +186,8 @@ __global__ void __launch_bounds__(32 * WARPS, BITS8 ? 5 : 4) adamw_multi_kernel(
   const int lane = threadIdx.x & 31;
   float* sm = turn[threadIdx.x >> 5];
   Hyper k = a.k;
+  pdl_launch();
+  pdl_wait();
   if (a.hp) {
     k.lr = a.hp[0];
     k.bc1 = a.hp[1];
@@ -315,6 +318,8 @@ __global__ void adamw_values_kernel(const uint8_t* __restrict__ m, const uint8_t
                                     const float* __restrict__ m_scale, const float* __restrict__ v_scale, long long blocks,
                                     uint16_t* __restrict__ mo, uint16_t* __restrict__ vo) {
   const long long b = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  pdl_launch();
+  pdl_wait();
   if (b >= blocks) return;
   const long long at = b * BLOCK + (threadIdx.x & 31) * 8;
   const uint2 mq = *reinterpret_cast<const uint2*>(m + at), vq = *reinterpret_cast<const uint2*>(v + at);
@@ -327,11 +332,8 @@ __global__ void adamw_values_kernel(const uint8_t* __restrict__ m, const uint8_t
 }
 
 template <typename P, typename G>
-void launch(const AdamArgs& a, bool bits8, unsigned grid, cudaStream_t st) {
-  if (bits8)
-    adamw_multi_kernel<P, G, true><<<grid, 32 * WARPS, 0, st>>>(a);
-  else
-    adamw_multi_kernel<P, G, false><<<grid, 32 * WARPS, 0, st>>>(a);
+cudaError_t launch(const AdamArgs& a, bool bits8, unsigned grid, cudaStream_t st) {
+  return pdl_start_one(bits8 ? adamw_multi_kernel<P, G, true> : adamw_multi_kernel<P, G, false>, grid, 32 * WARPS, 0, st, a);
 }
 
 }  // namespace
@@ -378,12 +380,10 @@ cudaError_t adamw_multi_launch(const soup_adamw_tensor* tensors, int count, cons
       a.hint[k] = static_cast<uint16_t>(i);
     }
     const unsigned grid = static_cast<unsigned>((a.blocks + WARPS - 1) / WARPS);
-    if (p_bf16)
-      g_bf16 ? launch<uint16_t, uint16_t>(a, m_scale != nullptr, grid, st) : launch<uint16_t, float>(a, m_scale != nullptr, grid, st);
-    else
-      g_bf16 ? launch<float, uint16_t>(a, m_scale != nullptr, grid, st) : launch<float, float>(a, m_scale != nullptr, grid, st);
-    ++g_kernel_launches;
-    const cudaError_t e = cudaGetLastError();
+    const bool bits8 = m_scale != nullptr;
+    const cudaError_t e =
+        p_bf16 ? (g_bf16 ? launch<uint16_t, uint16_t>(a, bits8, grid, st) : launch<uint16_t, float>(a, bits8, grid, st))
+               : (g_bf16 ? launch<float, uint16_t>(a, bits8, grid, st) : launch<float, float>(a, bits8, grid, st));
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -393,9 +393,7 @@ cudaError_t adamw_values_launch(const uint8_t* m, const uint8_t* v, const float*
                                 uint16_t* mo, uint16_t* vo, cudaStream_t st) {
   const long long blocks = n / BLOCK;
   if (blocks <= 0) return cudaSuccess;
-  adamw_values_kernel<<<static_cast<unsigned>((blocks + 7) / 8), 256, 0, st>>>(m, v, m_scale, v_scale, blocks, mo, vo);
-  ++g_kernel_launches;
-  return cudaGetLastError();
+  return pdl_start(adamw_values_kernel, static_cast<unsigned>((blocks + 7) / 8), 256, 0, st, m, v, m_scale, v_scale, blocks, mo, vo);
 }
 
 }  // namespace soup

@@ -27,6 +27,7 @@
 // states (onto whole 128-byte lines), so a half-masked batch costs half.
 #include "common.cuh"
 #include "internal.h"
+#include "pdl.cuh"
 #include "tc.cuh"
 
 #include <algorithm>
@@ -157,11 +158,6 @@ __device__ __forceinline__ bool group_all(int group, bool ok) {
 }
 // Barrier of one group of four epilogue warps.
 __device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
-// Programmatic dependent launch: a kernel may be set up while the one before it ends; it touches
-// nothing before that one's results are there.
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // K ranges of the gradient's tiles, each with an accumulator of its own.  A range costs its k-blocks and
 // about 10 more for its epilogue; pairs that idle cost time only below 93 % of them at work, because
 // the clock rises under the power limit when fewer work.  Measured, 1 / 2 / 3 ranges: 1108 / 901 / 977 us
@@ -1289,24 +1285,6 @@ int row_threads(int h) { return std::max(32, std::min(512, (h / 8 + 31) / 32 * 3
     if (e_ != cudaSuccess) return e_;     \
   } while (0)
 
-// A launch that may be set up while the one before it on the stream ends (every kernel here waits for
-// that one's results before it touches memory).
-template <typename... Params, typename... Args>
-cudaError_t launch(void (*kernel)(Params...), int grid, int threads, int smem, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3(static_cast<unsigned>(grid));
-  c.blockDim = dim3(static_cast<unsigned>(threads));
-  c.dynamicSmemBytes = static_cast<size_t>(smem);
-  c.stream = st;
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &a;
-  c.numAttrs = 1;
-  ++g_kernel_launches;
-  return cudaLaunchKernelEx(&c, kernel, static_cast<Params>(args)...);
-}
-
 cudaError_t gemm_attributes() {
   // once for each device; setting them twice at the same time does no harm
   static std::atomic<unsigned long long> done{0};
@@ -1359,7 +1337,7 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
     const CeRows rows = rows_of(q, base);
     int* n_rows = reinterpret_cast<int*>(base + q.n_rows);
     float* acc = reinterpret_cast<float*>(base + q.acc);
-    CE_CK(launch(ce_prepare_kernel, n, std::max(64, row_threads(H)), 0, st, h + t0 * ldh, ldh, w, ldw, n, H, V, t1 + t0,
+    CE_CK(pdl_start(ce_prepare_kernel, n, std::max(64, row_threads(H)), 0, st, h + t0 * ldh, ldh, w, ldw, n, H, V, t1 + t0,
                  t2 ? t2 + t0 : nullptr, packed, q.ld_packed, rows, reinterpret_cast<int*>(base + q.place), n_rows, q.splits, raised,
                  q.pieces,
                  lse ? lse + t0 : nullptr, logp + t0, logp2 ? logp2 + t0 : nullptr, err));
@@ -1396,7 +1374,7 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
       c.P = P;
       c.ldp = ldp;
       c.err = d.err = err;
-      CE_CK(launch(ce_narrow_kernel<false>, std::min(2 * q.pairs, c.n_tiles), THREADS, NARROW_SMEM, st, c));
+      CE_CK(pdl_start(ce_narrow_kernel<false>, std::min(2 * q.pairs, c.n_tiles), THREADS, NARROW_SMEM, st, c));
       if (grad) {
         d.ta = b.tb;
         d.n_tiles = (H + NARROW - 1) / NARROW;
@@ -1405,7 +1383,7 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
         d.acc = acc;
         d.with_stats = 1;
         d.stats = stats;
-        CE_CK(launch(ce_narrow_kernel<true>, 2 * q.pairs, THREADS, NARROW_SMEM, st, d));
+        CE_CK(pdl_start(ce_narrow_kernel<true>, 2 * q.pairs, THREADS, NARROW_SMEM, st, d));
       }
     }
     for (int i = 0; i < q.pieces && !q.narrow; ++i) {
@@ -1416,15 +1394,15 @@ cudaError_t linear_ce_fwd_launch(const uint16_t* h, long long ldh, const uint16_
       a.cols = std::min(V - a.w_row0, a.n_tiles * TILE);
       a.raised = raised + 2 * i;
       a.acc = i > 0 ? acc : nullptr;
-      CE_CK(launch(a.kb <= CHUNK ? ce_gemm_kernel<false, true> : ce_gemm_kernel<false, false>,
+      CE_CK(pdl_start(a.kb <= CHUNK ? ce_gemm_kernel<false, true> : ce_gemm_kernel<false, false>,
                    2 * std::min(q.pairs, mt * a.n_tiles), THREADS, SMEM_BYTES, st, a));
       if (!grad) continue;
       b.kb = (a.cols + BK - 1) / BK;
       b.accumulate = i > 0;
       b.with_stats = i == q.pieces - 1;
-      CE_CK(launch(ce_gemm_kernel<true, false>, 2 * q.pairs, THREADS, SMEM_BYTES, st, b));
+      CE_CK(pdl_start(ce_gemm_kernel<true, false>, 2 * q.pairs, THREADS, SMEM_BYTES, st, b));
     }
-    if (!grad) CE_CK(launch(ce_stats_kernel, (n + 3) / 4, 128, 0, st, n_rows, stats));
+    if (!grad) CE_CK(pdl_start(ce_stats_kernel, (n + 3) / 4, 128, 0, st, n_rows, stats));
   }
   return cudaSuccess;
 }
@@ -1437,7 +1415,7 @@ cudaError_t linear_ce_bwd_launch(const uint16_t* w, long long ldw, int T, int H,
     uint8_t* base = ws + k * q.per_block;
     // many accumulators a row: threads to share them
     const int threads = q.splits.of[(n + TILE - 1) / TILE] > 2 ? std::max(256, row_threads(H)) : row_threads(H);
-    CE_CK(launch(ce_dh_kernel, n, threads, threads * 32, st, reinterpret_cast<int*>(base + q.place), rows_of(q, base),
+    CE_CK(pdl_start(ce_dh_kernel, n, threads, threads * 32, st, reinterpret_cast<int*>(base + q.place), rows_of(q, base),
                  weight + t0, weight2 ? weight2 + t0 : nullptr, reinterpret_cast<float*>(base + q.acc),
                  reinterpret_cast<int*>(base + q.n_rows), w, ldw, H, dh + t0 * ldd, ldd));
   }

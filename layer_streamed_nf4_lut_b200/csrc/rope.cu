@@ -11,6 +11,7 @@
 // shared memory for each group 34.8), 32768 tokens of 72 heads, half of each rotated, 176 us (6.9 TB/s; 265).
 #include "common.cuh"
 #include "internal.h"
+#include "pdl.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -126,6 +127,8 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ R
     }
   };
   int h0 = u / a.items;
+  pdl_launch();
+  pdl_wait();
   fetch(h0);
   rope_angles(a, t0, tokens, cs, sn);
   float c[PAIRED ? 4 : 8], s[PAIRED ? 4 : 8];
@@ -187,6 +190,8 @@ __global__ void rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float cs[ROPE_MAX_PAIRS], sn[ROPE_MAX_PAIRS];
   const long long t = blockIdx.x;
   const int half = a.rotary / 2;
+  pdl_launch();
+  pdl_wait();
   rope_angles(a, t, 1, cs, sn);
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
@@ -276,7 +281,6 @@ cudaError_t rope_launch(const RopeCall& c, cudaStream_t st) {
   for (int i = 0; i < c.rotary / 2; ++i) a.turns[i] = c.freq[i] / 6.283185307179586476925;
   const int heads = c.heads[0] + c.heads[1];
   a.items = c.rotary / (c.interleaved ? 8 : 16) + (copies ? (c.head_dim - c.rotary) / 8 : 0);
-  ++g_kernel_launches;
   if (vec && a.items <= 256) {
     // as few rounds over the heads as 256 threads allow, and as many tokens in a block as then fit; one
     // token where that leaves SMs without a block
@@ -287,23 +291,15 @@ cudaError_t rope_launch(const RopeCall& c, cudaStream_t st) {
     a.tokens = std::max(1, std::min(256 / (a.items * a.rows), ROPE_BLOCK_ANGLES / (c.rotary / 2)));
     a.tokens = std::max(1, std::min(a.tokens, c.T / (2 * device_sm_count())));
     const int threads = (a.tokens * a.items * a.rows + 31) / 32 * 32;
-    const dim3 grid(static_cast<unsigned>((c.T + a.tokens - 1) / a.tokens));
-    if (c.f32)
-      c.interleaved ? rope_vec_kernel<float, true><<<grid, threads, 0, st>>>(a)
-                    : rope_vec_kernel<float, false><<<grid, threads, 0, st>>>(a);
-    else
-      c.interleaved ? rope_vec_kernel<uint16_t, true><<<grid, threads, 0, st>>>(a)
-                    : rope_vec_kernel<uint16_t, false><<<grid, threads, 0, st>>>(a);
-    return cudaGetLastError();
+    const unsigned grid = static_cast<unsigned>((c.T + a.tokens - 1) / a.tokens);
+    return pdl_start_one(c.f32 ? (c.interleaved ? rope_vec_kernel<float, true> : rope_vec_kernel<float, false>)
+                           : (c.interleaved ? rope_vec_kernel<uint16_t, true> : rope_vec_kernel<uint16_t, false>),
+                     grid, threads, 0, st, a);
   }
-  const dim3 grid(static_cast<unsigned>(c.T));
   const int threads = static_cast<int>(std::max(64ll, std::min(256ll, (1ll * heads * c.head_dim / 2 + 31) / 32 * 32)));
-  if (c.f32)
-    c.interleaved ? rope_kernel<float, true><<<grid, threads, 0, st>>>(a) : rope_kernel<float, false><<<grid, threads, 0, st>>>(a);
-  else
-    c.interleaved ? rope_kernel<uint16_t, true><<<grid, threads, 0, st>>>(a)
-                  : rope_kernel<uint16_t, false><<<grid, threads, 0, st>>>(a);
-  return cudaGetLastError();
+  return pdl_start_one(c.f32 ? (c.interleaved ? rope_kernel<float, true> : rope_kernel<float, false>)
+                         : (c.interleaved ? rope_kernel<uint16_t, true> : rope_kernel<uint16_t, false>),
+                   static_cast<unsigned>(c.T), threads, 0, st, a);
 }
 
 }  // namespace soup
