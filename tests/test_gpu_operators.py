@@ -588,3 +588,40 @@ def test_accumulated_gradients_of_the_same_index_twice():
     two = M.linear_ce(torch.cat((h, h)), w, torch.cat((t1, t1)), torch.cat((weight, weight)))
     for k in one:
         assert torch.equal(two[k][:40], one[k]) and torch.equal(two[k][40:], one[k]), k
+
+
+def test_loss_rows_past_32_bits_of_offset():
+    """Rows of h and of w whose places in memory need more than 32 bits."""
+    from layer_streamed_nf4_lut_b200 import model as M
+    T, H, V = 200, 64, 900
+    h, w, t1, weight = ce_inputs(T, H, V, 35)
+    want = M.linear_ce(h, w, t1, weight)
+    hs = torch.empty(T * 11_000_000, dtype=torch.bfloat16, device="cuda").as_strided((T, H), (11_000_000, 1))
+    hs.copy_(h)
+    got = M.linear_ce(hs, w, t1, weight)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    del hs
+    ws = torch.empty(V * 2_400_000, dtype=torch.bfloat16, device="cuda").as_strided((V, H), (2_400_000, 1))
+    ws.copy_(w)
+    for rows in (T, 60):
+        got = M.linear_ce(h[:rows], ws, t1[:rows].contiguous(), weight[:rows].contiguous())
+        want = M.linear_ce(h[:rows], w, t1[:rows].contiguous(), weight[:rows].contiguous())
+        assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+def test_adamw_of_more_than_2_to_the_31_elements():
+    from layer_streamed_nf4_lut_b200 import model as M
+    n, tail = (1 << 31) + 1000, 2280  # the tail starts on a block: n - tail is a multiple of 256
+    assert (n - tail) % 256 == 0
+    p, g = (torch.zeros(n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    some = torch.randn(tail, generator=gen(36), device="cuda").bfloat16()
+    p[-tail:] = some
+    g[-tail:] = some.flip(0) * 0.01
+    small_p, small_g = p[-tail:].clone(), g[-tail:].clone()
+    s, t = M.adamw_state([n], 8), M.adamw_state([tail], 8)
+    M.adamw_multi([p], [g], lr=1e-2, step=1, **s)
+    M.adamw_multi([small_p], [small_g], lr=1e-2, step=1, **t)
+    assert torch.equal(p[-tail:], small_p) and int((p[:-tail] != 0).sum()) == 0
+    k = t["m"].numel()
+    assert torch.equal(s["m"][-k:], t["m"]) and torch.equal(s["v"][-k:], t["v"])
+    assert torch.equal(s["m_scale"][-(k // 256):], t["m_scale"]) and torch.equal(s["v_scale"][-(k // 256):], t["v_scale"])
